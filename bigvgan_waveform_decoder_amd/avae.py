@@ -92,6 +92,16 @@ class avae_bwe_weights(ctypes.Structure):
     _fields_ = [("gen", avae_weights), ("forward_basis", P), ("mel_basis", P)]
 
 
+class avae_kv_q8(ctypes.Structure):
+    _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P),
+                ("n_pages", c_int), ("heads", c_int), ("page", c_int), ("dim", c_int)]
+
+
+class avae_ragged(ctypes.Structure):
+    _fields_ = [("cu", P), ("lens", P), ("table", P), ("table_ld", ctypes.c_longlong),
+                ("table_cols", c_int), ("seqs", c_int), ("total", c_int), ("max_rows", c_int)]
+
+
 _lib = None
 
 
@@ -192,6 +202,28 @@ def lib() -> ctypes.CDLL:
     L.avae_decoder_streaming_workspace_bytes.argtypes = [P, c_int, c_int, c_int]
     L.avae_bigvgan_decode_streaming.restype = c_int
     L.avae_bigvgan_decode_streaming.argtypes = [P, P, c_int, c_int, P, c_int, c_int, P, c_size_t, P]
+    LL = ctypes.c_longlong
+    L.avae_rms_norm_q8.restype = c_int
+    L.avae_rms_norm_q8.argtypes = [P, LL, P, LL, P, c_int, c_int, c_int, c_float, P, LL, P, LL, P,
+                                   P]
+    L.avae_quant_q8.restype = c_int
+    L.avae_quant_q8.argtypes = [P, LL, c_int, c_int, c_int, P, LL, P, P]
+    L.avae_dequant_q8.restype = c_int
+    L.avae_dequant_q8.argtypes = [P, LL, P, c_int, c_int, c_int, P, LL, P]
+    L.avae_linear_q8_workspace_bytes.restype = c_size_t
+    L.avae_linear_q8_workspace_bytes.argtypes = [c_int, c_int, c_int]
+    L.avae_linear_q8.restype = c_int
+    L.avae_linear_q8.argtypes = [P, LL, P, P, LL, P, P, c_int, c_int, c_int, c_int, c_int, P, LL,
+                                 P, c_size_t, P]
+    L.avae_kv_write_q8.restype = c_int
+    L.avae_kv_write_q8.argtypes = [P, LL, LL, P, LL, LL, c_int, P, P, P]
+    L.avae_kv_read_q8.restype = c_int
+    L.avae_kv_read_q8.argtypes = [P, P, c_int, P, P, P]
+    L.avae_attn_q8_workspace_bytes.restype = c_size_t
+    L.avae_attn_q8_workspace_bytes.argtypes = [P, P, c_int, c_int, c_int]
+    L.avae_attn_q8.restype = c_int
+    L.avae_attn_q8.argtypes = [P, LL, LL, c_int, c_int, P, P, P, c_int, c_float, c_int, c_int, P,
+                               P, P, c_size_t, P]
     L.avae_profile_begin.restype = c_int
     L.avae_profile_begin.argtypes = [c_int]
     L.avae_profile_end.restype = c_int
@@ -839,3 +871,231 @@ class BweDecoder:
                                             workspace.numel(), mel.data_ptr(), res.data_ptr(),
                                             _stream(stream)))
         return out, mel, res
+
+
+# ------------------------------------------------------------------ 8-bit serving operators
+
+ACT = {"none": 0, "silu": 1}
+_DTYPES: Dict = {}
+
+
+def _dtype_code(dtype) -> int:
+    if not _DTYPES:
+        torch = _torch()
+        _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    try:
+        return _DTYPES[dtype]
+    except KeyError:
+        raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}") from None
+
+
+def _rows(t, name: str, dtype, cols: Optional[int] = None, rows: Optional[int] = None):
+    """Pointer and row stride of a [rows, cols] device tensor whose last axis
+    is contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected two axes, got {tuple(t.shape)}")
+    m, n = t.shape
+    if (cols is not None and n != cols) or (rows is not None and m != rows):
+        raise ValueError(f"{name}: expected shape ({rows}, {cols}), got {(m, n)}")
+    ld, one = t.stride()
+    if one != 1 and n > 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    # the stride of a single row says nothing; torch may give any
+    return t.data_ptr(), (ld if m > 1 else max(ld, n))
+
+
+def _vec(t, name: str, n: int, dtype):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: must be {dtype}, got {t.dtype}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous vector of {n}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, stream=None):
+    """avae_rms_norm_q8: x [M, C] (+ residual) -> (q [M, C] int8, scale [M],
+    the sum in x's dtype or None)."""
+    torch = _torch()
+    M, C = x.shape
+    dt = _dtype_code(x.dtype)
+    px, ldx = _rows(x, "x", x.dtype)
+    dev = x.device
+    q = torch.empty((M, C), dtype=torch.int8, device=dev)
+    scale = torch.empty((M,), dtype=torch.float32, device=dev)
+    pr, ldr, total, pt = None, 0, None, None
+    if residual is not None:
+        pr, ldr = _rows(residual, "residual", x.dtype, C, M)
+        total = torch.empty((M, C), dtype=x.dtype, device=dev)
+        pt = total.data_ptr()
+    _check(lib().avae_rms_norm_q8(px, ldx, pr, ldr, _vec(weight, "weight", C, torch.float32), M, C,
+                                  dt, eps, pt, C, q.data_ptr(), C, scale.data_ptr(),
+                                  _stream(stream)))
+    return q, scale, total
+
+
+def quant_q8(x, stream=None):
+    """avae_quant_q8: x [M, C] -> (q [M, C] int8, scale [M])."""
+    torch = _torch()
+    M, C = x.shape
+    dt = _dtype_code(x.dtype)
+    px, ldx = _rows(x, "x", x.dtype)
+    q = torch.empty((M, C), dtype=torch.int8, device=x.device)
+    scale = torch.empty((M,), dtype=torch.float32, device=x.device)
+    _check(lib().avae_quant_q8(px, ldx, M, C, dt, q.data_ptr(), C, scale.data_ptr(),
+                               _stream(stream)))
+    return q, scale
+
+
+def dequant_q8(q, scale, dtype=None, stream=None):
+    """avae_dequant_q8: q [M, C] int8 with a scale a row -> [M, C] of dtype
+    (float32 if none is given)."""
+    torch = _torch()
+    dtype = torch.float32 if dtype is None else dtype
+    M, C = q.shape
+    pq, ldq = _rows(q, "q", torch.int8)
+    y = torch.empty((M, C), dtype=dtype, device=q.device)
+    _check(lib().avae_dequant_q8(pq, ldq, _vec(scale, "scale", M, torch.float32), M, C,
+                                 _dtype_code(dtype), y.data_ptr(), C, _stream(stream)))
+    return y
+
+
+def linear_q8(a, a_scale, w, w_scale, bias=None, act: str = "none", dtype=None, stream=None):
+    """avae_linear_q8: a [M, K] int8, w [N, K] int8 with a scale a row each
+    -> [M, N] of dtype (float32 if none is given)."""
+    torch = _torch()
+    dtype = torch.float32 if dtype is None else dtype
+    M, K = a.shape
+    N = w.shape[0]
+    pa, lda = _rows(a, "a", torch.int8)
+    pw, ldw = _rows(w, "w", torch.int8, K)
+    if act not in ACT:
+        raise ValueError(f"act must be one of {sorted(ACT)}, got {act!r}")
+    y = torch.empty((M, N), dtype=dtype, device=a.device)
+    L = lib()
+    need = L.avae_linear_q8_workspace_bytes(M, N, K)
+    ws = torch.empty((need,), dtype=torch.uint8, device=a.device) if need else None
+    _check(L.avae_linear_q8(pa, lda, _vec(a_scale, "a_scale", M, torch.float32), pw, ldw,
+                            _vec(w_scale, "w_scale", N, torch.float32),
+                            None if bias is None else _vec(bias, "bias", N, torch.float32),
+                            M, N, K, ACT[act], _dtype_code(dtype), y.data_ptr(), N,
+                            None if ws is None else ws.data_ptr(), need, _stream(stream)))
+    return y
+
+
+class KvCacheQ8:
+    """The four tensors of a paged 8-bit cache (avae_kv_q8): k, v [n_pages,
+    heads, page, dim] int8 and k_scale, v_scale [n_pages, heads] float32."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "c")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        for name, t, dtype, shape in (("k", k, torch.int8, k.shape), ("v", v, torch.int8, k.shape),
+                                      ("k_scale", k_scale, torch.float32, k.shape[:2]),
+                                      ("v_scale", v_scale, torch.float32, k.shape[:2])):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name}: must be a contiguous device tensor")
+            if t.dtype != dtype:
+                raise ValueError(f"{name}: must be {dtype}, got {t.dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if k.dim() != 4:
+            raise ValueError(f"k: expected [n_pages, heads, page, dim], got {tuple(k.shape)}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.c = avae_kv_q8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                            *k.shape)
+
+    @classmethod
+    def empty(cls, n_pages: int, heads: int, page: int, dim: int, device="cuda"):
+        """A cache with no token in it (what it holds does not matter: a page
+        is written from its first token on)."""
+        torch = _torch()
+        shape = (n_pages, heads, page, dim)
+        return cls(*(torch.zeros(shape, dtype=torch.int8, device=device) for _ in range(2)),
+                   *(torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _ragged(table, cu, lens, total: int, max_rows: int):
+    i32 = _torch().int32
+    if table.dim() != 2:
+        raise ValueError(f"table: expected [sequences, pages], got {tuple(table.shape)}")
+    seqs, cols = table.shape
+    pt, ld = _rows(table, "table", i32)
+    return avae_ragged(_vec(cu, "cu", seqs + 1, i32), _vec(lens, "lens", seqs, i32), pt, ld, cols,
+                       seqs, total, max_rows)
+
+
+def _heads(t, name: str, heads: Optional[int], dim: int):
+    """Pointer, token and head stride of a [tokens, heads, dim] tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name}: expected [tokens, {heads or 'heads'}, {dim}], "
+                         f"got {tuple(t.shape)}")
+    tok, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return t.data_ptr(), tok, head
+
+
+def kv_write_q8(cache: KvCacheQ8, k, v, table, cu, lens, max_new: Optional[int] = None,
+                stream=None):
+    """avae_kv_write_q8: k, v [tokens, heads, dim] into the cache's pages.
+    max_new: at least the most rows of one sequence (all of them if not given)."""
+    c = cache.c
+    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have one dtype and as many tokens")
+    total = k.shape[0]
+    rows = _ragged(table, cu, lens, total, total if max_new is None else min(max_new, total))
+    _check(lib().avae_kv_write_q8(*_heads(k, "k", c.heads, c.dim), *_heads(v, "v", c.heads, c.dim),
+                                  _dtype_code(k.dtype), ctypes.byref(c), ctypes.byref(rows),
+                                  _stream(stream)))
+
+
+def kv_read_q8(cache: KvCacheQ8, table, cu, lens, total: int, max_rows: Optional[int] = None,
+               dtype=None, stream=None):
+    """avae_kv_read_q8: the sequences' last tokens, `total` of them, as cu
+    says -> k, v [total, heads, dim] of dtype (float32 if none is given)."""
+    torch = _torch()
+    c = cache.c
+    dtype = torch.float32 if dtype is None else dtype
+    k, v = (torch.empty((total, c.heads, c.dim), dtype=dtype, device=cache.k.device)
+            for _ in range(2))
+    rows = _ragged(table, cu, lens, total, total if max_rows is None else min(max_rows, total))
+    _check(lib().avae_kv_read_q8(ctypes.byref(c), ctypes.byref(rows), _dtype_code(dtype),
+                                 k.data_ptr(), v.data_ptr(), _stream(stream)))
+    return k, v
+
+
+def attn_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = None,
+            max_len: Optional[int] = None, scale: Optional[float] = None, causal: bool = True,
+            window: int = 0, first=None, return_lse: bool = False, stream=None):
+    """avae_attn_q8: q [tokens, q_heads, dim] over the cache -> the same shape
+    (and lse [tokens, q_heads] float32 if asked for).  max_q: at least the most
+    rows of one sequence; max_len: at least the longest sequence (the table's
+    tokens if not given); scale: 1 / sqrt(dim) if not given."""
+    torch = _torch()
+    c = cache.c
+    pq, tok, head = _heads(q, "q", None, c.dim)
+    total, heads = q.shape[:2]
+    rows = _ragged(table, cu, lens, total, total if max_q is None else min(max_q, total))
+    if max_len is None:
+        max_len = rows.table_cols * c.page
+    out = torch.empty((total, heads, c.dim), dtype=q.dtype, device=q.device)
+    lse = torch.empty((total, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    L = lib()
+    pc, pr = ctypes.byref(c), ctypes.byref(rows)
+    need = L.avae_attn_q8_workspace_bytes(pc, pr, heads, max_len, window)
+    ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+    _check(L.avae_attn_q8(pq, tok, head, heads, _dtype_code(q.dtype), pc, pr,
+                          None if first is None else _vec(first, "first", rows.seqs, torch.int32),
+                          max_len, c.dim ** -0.5 if scale is None else scale, 1 if causal else 0,
+                          window, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                          None if ws is None else ws.data_ptr(), need, _stream(stream)))
+    return (out, lse) if return_lse else out

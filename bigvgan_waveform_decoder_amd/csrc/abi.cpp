@@ -182,6 +182,19 @@ int run_amp(const float* x, float* y, int B, int C, int T, int K, int n_dil, con
 // Small entry points
 // =========================================================================
 
+int avae::abi_fail(int code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    std::vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    try {
+        g_err = buf;
+    } catch (...) {  // no memory for the message: the code still tells
+    }
+    return code;
+}
+
 extern "C" const char* avae_last_error(void) { return g_err.c_str(); }
 
 extern "C" int avae_version(void) { return 100; }

@@ -137,4 +137,57 @@ hipError_t launch_stream_copy(const float* x, float* y, long long n4, hipStream_
 hipError_t launch_channel_affine(const float* x, float* y, const float* scale,
                                  const float* shift, int B, int C, int T, hipStream_t stream);
 
+// ---- 8-bit serving operators (q8_*.hip).  dtype: enum avae_dtype.
+
+// Sets the calling thread's avae_last_error() and returns `code`.
+int abi_fail(int code, const char* fmt, ...);
+
+// The paged cache and its page table, as include/avae.h describes them.
+struct CacheQ8 {
+    int8_t *k, *v;            // [n_pages][heads][page][dim]
+    float *k_scale, *v_scale; // [n_pages][heads]
+    const int* table;         // [seqs][table_ld], page of each column
+    long long table_ld;
+    int table_cols;
+    int n_pages, heads, page, dim;
+};
+
+// Packed rows of `seqs` sequences: rows cu[b] .. cu[b+1] are the last ones of
+// sequence b, which has lens[b] tokens.
+struct Ragged {
+    const int *cu, *lens;
+    int seqs, total, max_rows;
+};
+
+// sum, res and w may be null (no residual; no norm).
+hipError_t launch_rows_q8(int dtype, const void* x, long long ldx, const void* res, long long ldr,
+                          const float* w, int M, int C, float eps, void* sum, long long lds,
+                          int8_t* q, long long ldq, float* scale, hipStream_t stream);
+hipError_t launch_dequant_q8(int dtype, const int8_t* q, long long ldq, const float* scale, int M,
+                             int C, void* y, long long ldy, hipStream_t stream);
+size_t linear_q8_workspace_bytes(int M, int N, int K);
+hipError_t launch_linear_q8(const int8_t* a, long long lda, const float* sa, const int8_t* w,
+                            long long ldw, const float* sw, const float* bias, int M, int N, int K,
+                            int act, int dtype, void* y, long long ldy, void* ws,
+                            hipStream_t stream);
+hipError_t launch_kv_write_q8(int dtype, const void* k, long long k_tok, long long k_head,
+                              const void* v, long long v_tok, long long v_head, const CacheQ8& c,
+                              const Ragged& r, hipStream_t stream);
+hipError_t launch_kv_read_q8(int dtype, const CacheQ8& c, const Ragged& r, void* k, void* v,
+                             hipStream_t stream);
+
+struct AttnQ8 {
+    const void* q;            // [total][q_heads][dim], strides q_tok, q_head
+    long long q_tok, q_head;
+    void* out;                // [total][q_heads][dim]
+    float* lse;               // [total][q_heads] or null
+    const int* first;         // [seqs] or null: keys before it are not seen
+    int q_heads, max_len, causal, window;
+    float scale;
+};
+size_t attn_q8_workspace_bytes(int seqs, int max_rows, int max_len, int q_heads, int heads,
+                               int dim, int window);
+hipError_t launch_attn_q8(int dtype, const AttnQ8& a, const CacheQ8& c, const Ragged& r, void* ws,
+                          hipStream_t stream);
+
 }  // namespace avae

@@ -495,6 +495,159 @@ int avae_bwe_decode_traced(const avae_bwe* bwe, const float* low, int B, int T, 
                            void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * 8-bit serving operators of an autoregressive latent generator, the network
+ * that writes the decoder's latent frames one after the other: norm, product,
+ * paged cache and attention with 8-bit operands.
+ *
+ * Tensors here have the type that `dtype` names (float32, bfloat16 or
+ * float16) or, where the declaration says so, 8 bits, float32 or int32.
+ * Strides are in elements; the last axis is contiguous.  All arithmetic is
+ * in float32 (sums of 8-bit products in int32) whatever the type, and each
+ * output is rounded to it once.  A call with nothing to do (M = 0, no
+ * sequences, no rows) succeeds without a launch.
+ *
+ * An 8-bit value q in [-127, 127] with scale s stands for q * s.
+ * ---------------------------------------------------------------------------
+ */
+enum avae_dtype { AVAE_F32 = 0, AVAE_BF16 = 1, AVAE_F16 = 2 };
+enum avae_act { AVAE_ACT_NONE = 0, AVAE_ACT_SILU = 1 };
+
+/*
+ * Root-mean-square norm with the residual's addition and an 8-bit output:
+ *   h = x + residual (x alone if residual is NULL), kept in float32;
+ *   sum = h rounded to dtype (given exactly when residual is);
+ *   v = h * weight;  s = max_c |v| / 127;  q = rint(v / s), ties to even;
+ *   scale = s / sqrt(mean_c(h^2) + eps):
+ * q * scale is the normed row.  A row of zeros (or one whose s underflows)
+ * has q = 0 and scale = 0; a row whose v holds a NaN or an infinity has
+ * q = 0 and scale = NaN.
+ *   x, residual, sum: [M, C] at row strides ldx, ldr, ldsum; sum must
+ *   overlap neither.  weight: [C] float32.  q: [M, C] 8-bit at ldq.
+ *   scale: [M] float32.
+ * avae_quant_q8 is the row quantiser alone (v = x, scale = s).
+ * avae_dequant_q8 reads rows back: y = q * scale.
+ * Errors: EINVAL (null or misaligned pointer, M < 0, C < 1, dtype, eps
+ *   negative or not finite, only one of residual and sum); ESHAPE (a row
+ *   stride under C).
+ */
+int avae_rms_norm_q8(const void* x, long long ldx, const void* residual, long long ldr,
+                     const float* weight, int M, int C, int dtype, float eps, void* sum,
+                     long long ldsum, signed char* q, long long ldq, float* scale, void* stream);
+int avae_quant_q8(const void* x, long long ldx, int M, int C, int dtype, signed char* q,
+                  long long ldq, float* scale, void* stream);
+int avae_dequant_q8(const signed char* q, long long ldq, const float* scale, int M, int C,
+                    int dtype, void* y, long long ldy, void* stream);
+
+/*
+ * Product of 8-bit rows:
+ *   y[m, n] = act( (sum_k a[m, k] w[n, k]) * a_scale[m] * w_scale[n] + bias[n] )
+ * the sum in int32 (exact), the rest in float32.
+ *   a: [M, K] 8-bit at row stride lda; w: [N, K] 8-bit at ldw (the layout of
+ *   a linear layer's weight); a_scale [M], w_scale [N], bias [N] (or NULL)
+ *   float32; y: [M, N] of dtype at ldy; act: enum avae_act (SiLU is
+ *   v / (1 + exp(-v))).  Any K up to AVAE_LINEAR_Q8_MAX_K and any strides;
+ *   bases and strides that are multiples of 16 bytes are fastest.
+ *   workspace: device, avae_linear_q8_workspace_bytes(M, N, K) (which may
+ *   be 0) bytes, aligned to 16; its contents do not matter.
+ * Errors: EINVAL, ESHAPE (K or a stride out of range), EWORKSPACE.
+ */
+#define AVAE_LINEAR_Q8_MAX_K 131071
+size_t avae_linear_q8_workspace_bytes(int M, int N, int K);
+int avae_linear_q8(const signed char* a, long long lda, const float* a_scale, const signed char* w,
+                   long long ldw, const float* w_scale, const float* bias, int M, int N, int K,
+                   int act, int dtype, void* y, long long ldy, void* workspace, size_t ws_bytes,
+                   void* stream);
+
+/*
+ * A paged cache of keys and values in 8 bits, with one float32 scale for
+ * each page and head.
+ *   k, v: [n_pages, heads, page, dim] 8-bit, aligned to 16 bytes;
+ *   k_scale, v_scale: [n_pages, heads] float32.
+ *   page: tokens a page, one of 16, 32, 64, 128, 256; dim: 64, 128 or 256.
+ */
+typedef struct avae_kv_q8 {
+    signed char* k;
+    signed char* v;
+    float* k_scale;
+    float* v_scale;
+    int n_pages, heads, page, dim;
+} avae_kv_q8;
+
+/*
+ * Packed rows of `seqs` sequences (all pointers DEVICE memory, int32).
+ *   cu [seqs + 1]: rows cu[b] .. cu[b+1] of the packed tensors are the LAST
+ *     cu[b+1] - cu[b] tokens of sequence b, in order; none if they are equal.
+ *   lens [seqs]: tokens of sequence b, these rows among them.
+ *   table [seqs, table_cols] at row stride table_ld: the page that holds
+ *     tokens j*page .. (j+1)*page - 1 of the sequence.  Entries past a
+ *     sequence's length are not read.
+ *   total: rows of the packed tensors; max_rows: at least the most rows of
+ *     one sequence (rows past it are not computed).
+ * The kernels check what the host cannot see: rows outside 0 .. total, a
+ * table column past table_cols or an entry that is no page leave that token
+ * out (not written; zeros when read; not seen by the attention).
+ */
+typedef struct avae_ragged {
+    const int* cu;
+    const int* lens;
+    const int* table;
+    long long table_ld;
+    int table_cols;
+    int seqs, total, max_rows;
+} avae_ragged;
+
+/*
+ * Quantise new keys and values as they are written.  For each page and head,
+ * with new tokens x: if the page held no token of the sequence, its scale
+ * becomes max|x| / 127; else it becomes the larger of that and what it was,
+ * and where it grew the held values move to it, q' = rint(q * old / new).
+ * Then q = rint(x / scale), ties to even.  Writing the same tokens again
+ * changes nothing.  A NaN or an infinity among the new tokens makes that
+ * page's scale for that head NaN, and it stays NaN until the page is written
+ * from its first token on.  Sequences must not share a page that is written.
+ *   k, v: [total, heads, dim] of dtype at token strides k_tok, v_tok and
+ *   head strides k_head, v_head.
+ * avae_kv_read_q8 reads rows back: k, v [total, heads, dim] contiguous, of
+ *   dtype; the rows are the sequences' last tokens as `rows` says.
+ * Errors: EINVAL, ESHAPE.
+ */
+int avae_kv_write_q8(const void* k, long long k_tok, long long k_head, const void* v,
+                     long long v_tok, long long v_head, int dtype, const avae_kv_q8* cache,
+                     const avae_ragged* rows, void* stream);
+int avae_kv_read_q8(const avae_kv_q8* cache, const avae_ragged* rows, int dtype, void* k, void* v,
+                    void* stream);
+
+/*
+ * Attention of packed query rows over the cache, the rows' own tokens among
+ * the keys (write them first).  A row at position p of its sequence sees the
+ * keys t with first[b] <= t < lens[b], with `causal` t <= p, and with
+ * window > 0 (causal only) t > p - window:
+ *   out = sum_t softmax_t(scale * q . k_t) v_t.
+ * Query head h reads cache head h / (q_heads / heads).  A row that sees
+ * nothing gives zeros, and -inf in lse.
+ *   q: [total, q_heads, dim] of dtype at strides q_tok, q_head; out: the
+ *   same, contiguous.  lse: [total, q_heads] float32 (the natural logarithm
+ *   of the sum of exponentials) or NULL.  first: [seqs] int32 or NULL (0).
+ *   max_len: at least the largest of lens (longer sequences' results are
+ *   not defined, but nothing outside the buffers is touched).
+ *   workspace: device, avae_attn_q8_workspace_bytes(..) (which may be 0)
+ *   bytes, aligned to 16; its contents do not matter.  Of `rows` and
+ *   `cache` the query reads only the sizes.
+ * float32 queries are multiplied with 22 of their 24 bits, and so are the
+ * probabilities for float32 output (11 for 16-bit outputs), down to 2^-40 of
+ * the row's largest probability and value scale; the sums are float32.
+ * Errors: EINVAL, ESHAPE (head counts, dim, page, max_len over the table),
+ *   EWORKSPACE.
+ */
+size_t avae_attn_q8_workspace_bytes(const avae_kv_q8* cache, const avae_ragged* rows, int q_heads,
+                                    int max_len, int window);
+int avae_attn_q8(const void* q, long long q_tok, long long q_head, int q_heads, int dtype,
+                 const avae_kv_q8* cache, const avae_ragged* rows, const int* first, int max_len,
+                 float scale, int causal, int window, void* out, float* lse, void* workspace,
+                 size_t ws_bytes, void* stream);
+
+/*
  * Launch profiler, the device-side counterpart of the audio decoder's own
  * phase report ([H3] AVAE_TIME / avae_time_report, phases dec_in, conv_pre,
  * upsamples, resblocks, act_post, conv_post).  Between avae_profile_begin and
