@@ -65,6 +65,13 @@ __device__ inline int page_of(const CacheQ8& c, int b, int col) {
     return page >= 0 && page < c.n_pages ? page : -1;
 }
 
+// Workgroups go to the 8 XCDs in turn; this gives each XCD a contiguous range
+// of the `count` tiles, so that neighbours share its L2.
+__device__ inline int xcd_remap(int id, int count) {
+    const int q = count >> 3, r = count & 7, xcd = id & 7, at = id >> 3;
+    return xcd < r ? xcd * (q + 1) + at : r * (q + 1) + (xcd - r) * q + at;
+}
+
 __device__ inline unsigned wave_max(unsigned v) {
     for (int o = 32; o > 0; o >>= 1) v = max(v, (unsigned)__shfl_xor((int)v, o));
     return v;
