@@ -185,8 +185,8 @@ struct AttnQ8 {
     int q_heads, max_len, causal, window;
     float scale;
 };
-size_t attn_q8_workspace_bytes(int seqs, int max_rows, int max_len, int q_heads, int heads,
-                               int dim, int window);
+size_t attn_q8_workspace_bytes(int seqs, int total, int max_rows, int max_len, int q_heads,
+                               int heads, int dim, int window);
 hipError_t launch_attn_q8(int dtype, const AttnQ8& a, const CacheQ8& c, const Ragged& r, void* ws,
                           hipStream_t stream);
 

@@ -627,7 +627,7 @@ int avae_kv_read_q8(const avae_kv_q8* cache, const avae_ragged* rows, int dtype,
  * Query head h reads cache head h / (q_heads / heads).  A row that sees
  * nothing gives zeros, and -inf in lse.
  *   q: [total, q_heads, dim] of dtype at strides q_tok, q_head; out: the
- *   same, contiguous.  lse: [total, q_heads] float32 (the natural logarithm
+ *   same, contiguous, aligned to four elements.  lse: [total, q_heads] float32 (the natural logarithm
  *   of the sum of exponentials) or NULL.  first: [seqs] int32 or NULL (0).
  *   max_len: at least the largest of lens (longer sequences' results are
  *   not defined, but nothing outside the buffers is touched).

@@ -557,3 +557,37 @@ def test_attention_reads_the_cache_in_any_page_order():
                     dtype=torch.float32).bfloat16()
     outs = [x.avae.attn_q8(q, x.upload(), _dev(x.table), _dev(cu), _dev(x.lens)) for x in (a, b)]
     assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,lens,heads,kv_heads,dim,page", [
+    ([1, 1, 1], [3000, 1, 1777], 4, 2, 64, 16), ([1], [9001], 2, 1, 128, 64),
+    ([4, 2], [5000, 130], 12, 4, 128, 32), ([1, 1], [2500, 2048], 3, 1, 256, 128)])
+def test_attention_long(new, lens, heads, kv_heads, dim, page, dtype):
+    """Few rows over many keys: the keys are split and joined."""
+    announce(f"attn_q8 long {new} {lens} {heads}/{kv_heads} dim {dim} page {page} {dtype}")
+    c = Cache(31, lens, kv_heads, dim, page)
+    c.poison_unused()
+    _check_attention(c, new, heads, dtype, 9)
+    _check_attention(c, new, heads, dtype, 9, window=1000)
+    _check_attention(c, new, heads, dtype, 9,
+                     first=np.array([2000] * len(lens), np.int32))
+
+
+def test_attention_pages_next_to_the_seen_keys_may_hold_anything():
+    """Pages outside the window, in the same 32 keys as seen ones, with
+    scales of NaN, infinity and the largest float32."""
+    announce("attn_q8 neighbours")
+    new, lens = [1, 1], [115, 400]
+    for bad in (np.nan, np.inf, 3e38):
+        c = Cache(32, lens, 1, 64, 16)
+        c.poison_unused()
+        for b, lo in ((0, 112), (1, 304)):  # windows of 3 and 96 keys
+            for col in range(lo // 16):
+                c.ks[c.table[b, col]] = bad
+                c.vs[c.table[b, col]] = bad
+        c.table = np.concatenate([c.table, np.full((2, 1), c.spare[0], np.int32)], 1)
+        c.ks[c.spare[0]] = c.vs[c.spare[0]] = bad
+        c.table[0, 8] = c.spare[0]  # past the first sequence's length
+        for dtype in ("f32", "bf16"):
+            _check_attention(c, new, 2, dtype, 3, first=np.array([112, 304], np.int32))
