@@ -66,6 +66,7 @@ int check_cache(const char* who, const avae_kv_q8* kv, CacheQ8* out) {
     out->n_pages = kv->n_pages;
     out->heads = kv->heads;
     out->page = kv->page;
+    for (out->shift = 4; 1 << out->shift < kv->page;) ++out->shift;
     out->dim = kv->dim;
     return AVAE_OK;
 }

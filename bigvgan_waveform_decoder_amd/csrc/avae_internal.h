@@ -150,6 +150,7 @@ struct CacheQ8 {
     long long table_ld;
     int table_cols;
     int n_pages, heads, page, dim;
+    int shift;                // page = 1 << shift
 };
 
 // Packed rows of `seqs` sequences: rows cu[b] .. cu[b+1] are the last ones of

@@ -58,11 +58,19 @@ __device__ inline bool ragged_rows(const Ragged& r, int b, int& at, int& n, int&
 }
 
 // The page of a table's column, or -1 if there is none: a column outside the
-// table, or an entry that is no page.
+// table, or an entry that is no page.  In two steps, so that an entry can be
+// on its way while other work goes on; the entry is read from inside the
+// table whatever the column (col >= 0).
+__device__ inline int page_entry(const CacheQ8& c, int b, int col) {
+    return c.table[(long long)b * c.table_ld + min(col, c.table_cols - 1)];
+}
+
+__device__ inline int page_checked(const CacheQ8& c, int col, int entry) {
+    return col < c.table_cols && entry >= 0 && entry < c.n_pages ? entry : -1;
+}
+
 __device__ inline int page_of(const CacheQ8& c, int b, int col) {
-    if (col < 0 || col >= c.table_cols) return -1;
-    const int page = c.table[(long long)b * c.table_ld + col];
-    return page >= 0 && page < c.n_pages ? page : -1;
+    return page_checked(c, col, page_entry(c, b, col));
 }
 
 // Workgroups go to the 8 XCDs in turn; this gives each XCD a contiguous range
@@ -70,6 +78,11 @@ __device__ inline int page_of(const CacheQ8& c, int b, int col) {
 __device__ inline int xcd_remap(int id, int count) {
     const int q = count >> 3, r = count & 7, xcd = id & 7, at = id >> 3;
     return xcd < r ? xcd * (q + 1) + at : r * (q + 1) + (xcd - r) * q + at;
+}
+
+// This wave's index in its workgroup, known to be the same in all its lanes.
+__device__ inline int wave_id() {
+    return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
 }
 
 __device__ inline unsigned wave_max(unsigned v) {

@@ -35,11 +35,26 @@ using namespace q8;
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ inline float neg_inf() { return __uint_as_float(0xff800000u); }
+__device__ inline float nan() { return __uint_as_float(0x7fc00000u); }
+__device__ inline bool finite(float x) { return fabsf(x) < __uint_as_float(0x7f800000u); }
+
+// The larger of a lane's value and that of the lane 32 (16) further on.
+__device__ inline float max_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                    false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ inline float max_quarters(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                    false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 
 // Natural logarithm of a sum of exponentials held as 2^m * l.
 __device__ inline float lse_of(float m, float l) {
@@ -53,11 +68,21 @@ __device__ inline h2 to_half2(unsigned bytes, unsigned sel) {
     return __builtin_bit_cast(h2, u) - (h2){(_Float16)1152, (_Float16)1152};
 }
 
-// Eight 8-bit values (two words, each already xor 0x80808080) in float16.
+// Eight stored values (two words) in float16.
 __device__ inline h8 to_half8(unsigned lo, unsigned hi) {
+    lo ^= 0x80808080u;
+    hi ^= 0x80808080u;
     h2 r[4] = {to_half2(lo, 0x04010400u), to_half2(lo, 0x04030402u), to_half2(hi, 0x04010400u),
                to_half2(hi, 0x04030402u)};
     return __builtin_bit_cast(h8, r);
+}
+
+// Bytes 0, 1 (2, 3) of two keys' words, key by key, with the same offset.
+__device__ inline unsigned pair_lo(unsigned a, unsigned b) {
+    return __builtin_amdgcn_perm(b, a, 0x05010400u) ^ 0x80808080u;
+}
+__device__ inline unsigned pair_hi(unsigned a, unsigned b) {
+    return __builtin_amdgcn_perm(b, a, 0x07030602u) ^ 0x80808080u;
 }
 
 template <int N>
@@ -66,14 +91,14 @@ struct Words {
 };
 
 template <int N>
-__device__ inline Words<N> load_bytes(const int8_t* p) {  // 4 N bytes, 4 N-byte aligned
+__device__ inline Words<N> load_words(const int8_t* p) {  // 4 N bytes, 4 N-byte aligned
     struct alignas(4 * N) Raw {
         unsigned w[N];
     };
     const Raw raw = *reinterpret_cast<const Raw*>(p);
     Words<N> r;
 #pragma unroll
-    for (int i = 0; i < N; ++i) r.w[i] = raw.w[i] ^ 0x80808080u;
+    for (int i = 0; i < N; ++i) r.w[i] = raw.w[i];
     return r;
 }
 
@@ -167,7 +192,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, Cach
     constexpr int LD = D + 4;
     __shared__ float s_out[kWaves * 16 * LD];
     __shared__ float s_m[kWaves * 16], s_l[kWaves * 16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n16 = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = wave_id(), n16 = lane & 15, g = lane >> 4;
     const int b = blockIdx.z, head = blockIdx.y;
     const int split = blockIdx.x % splits, tile = blockIdx.x / splits;
     int cu0, n, len;
@@ -189,6 +214,13 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, Cach
 
     f4 acc[DT] = {};
     float m = neg_inf(), l = 0.0f, v_run = 0.0f;
+    // the table entries of a step, read a step ahead of their use
+    int entry[2];
+    auto look_up = [&](int t0) {
+        entry[0] = page_entry(c, b, t0 >> c.shift);
+        entry[1] = page_entry(c, b, (t0 + 16) >> c.shift);
+    };
+    look_up(t_lo + 32 * wave);
     for (int t0 = t_lo + 32 * wave; t0 < t_hi; t0 += 32 * kWaves) {
         f4 s[2];
         float vs[2];
@@ -199,21 +231,22 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, Cach
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int k0 = t0 + 16 * h;
-            const int page = page_of(c, b, k0 / c.page);
+            const int page = page_checked(c, k0 >> c.shift, entry[h]);
             // a half that no row sees may lie in a page that holds anything
             there[h] = page >= 0 && k0 < any_hi && k0 + 16 > any_lo;
             const long long at = (long long)max(page, 0) * c.heads + head;
-            const int8_t* kp = c.k + (at * c.page + k0 % c.page) * D;
-            const int8_t* vp = c.v + (at * c.page + k0 % c.page) * D;
+            const int8_t* kp = c.k + (at * c.page + (k0 & (c.page - 1))) * D;
+            const int8_t* vp = c.v + (at * c.page + (k0 & (c.page - 1))) * D;
 #pragma unroll
             for (int j = 0; j < D / 64; ++j)
-                kw[h][j] = load_bytes<4>(kp + n16 * D + 64 * j + 16 * g);
+                kw[h][j] = load_words<4>(kp + n16 * D + 64 * j + 16 * g);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                vw[4 * h + i] = load_bytes<D / 64>(vp + (4 * g + i) * D + (D / 16) * n16);
+                vw[4 * h + i] = load_words<D / 64>(vp + (4 * g + i) * D + (D / 16) * n16);
             ks[h] = c.k_scale[at];
             vs[h] = c.v_scale[at];
         }
+        look_up(t0 + 32 * kWaves);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             f4 sum = {};
@@ -231,29 +264,29 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, Cach
             }
             s[h] = sum * (ks[h] * to_log2);
         }
-        // keys that not every row sees, or that are not there
-        const bool whole = there[0] && there[1] && t0 >= all_lo && t0 + 32 <= all_hi;
-        unsigned hidden = 0;
-        if (!whole) {
+        if (__builtin_amdgcn_readfirstlane(t0 < all_lo || t0 + 32 > all_hi || !there[0] ||
+                                           !there[1] || !finite(vs[0] + vs[1]))) {
+            // Some of the keys are hidden from some of the rows, or a page's
+            // value scale is NaN: that goes into the scores, so that it stays
+            // with the rows that see it.
+            const int lo = row.lo - t0 - 4 * g, hi = row.hi - t0 - 4 * g;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int key = t0 + 16 * h + 4 * g + i;
-                    if (!(there[h] && key >= row.lo && key < row.hi)) {
-                        hidden |= 1u << (4 * h + i);
-                        s[h][i] = neg_inf();
-                    }
+                    s[h][i] += finite(vs[h]) ? 0.0f : nan();
+                    s[h][i] = there[h] && 16 * h + i >= lo && 16 * h + i < hi ? s[h][i] : neg_inf();
                 }
+                vs[h] = there[h] && finite(vs[h]) ? vs[h] : 0.0f;
+            }
         }
         float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                           fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
+        top = max_halves(max_quarters(top));
         const float m_new = fmaxf(m, top);
         const float m_at = m_new == neg_inf() ? 0.0f : m_new;
         // the largest value scale so far stands at 2^15
-        const float v_new = fmaxf(v_run, fmaxf(there[0] ? vs[0] : 0.0f, there[1] ? vs[1] : 0.0f));
+        const float v_new = fmaxf(v_run, fmaxf(vs[0], vs[1]));
         const float inv = 1.0f / fmaxf(v_new, 1e-38f);
         float back = __builtin_amdgcn_exp2f(m - m_at);
         l *= back;
@@ -272,9 +305,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, Cach
             for (int i = 0; i < 4; ++i) {
                 const float p = __builtin_amdgcn_exp2f(s[h][i] - m_at);
                 l += p;
-                float x = p * pv;
-                // a page's NaN scale stays with the rows that see it
-                if (!whole && (hidden >> (4 * h + i) & 1)) x = 0.0f;
+                const float x = p * pv;
                 const _Float16 hx = (_Float16)x;
                 ph[4 * h + i] = hx;
                 if (kSplit) pl[4 * h + i] = (_Float16)(x - (float)hx);
@@ -286,8 +317,8 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, Cach
             unsigned lo01[4], hi01[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                lo01[i] = __builtin_amdgcn_perm(vw[2 * i + 1].w[w], vw[2 * i].w[w], 0x05010400u);
-                hi01[i] = __builtin_amdgcn_perm(vw[2 * i + 1].w[w], vw[2 * i].w[w], 0x07030602u);
+                lo01[i] = pair_lo(vw[2 * i].w[w], vw[2 * i + 1].w[w]);
+                hi01[i] = pair_hi(vw[2 * i].w[w], vw[2 * i + 1].w[w]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -354,6 +385,354 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, Cach
     }
 }
 
+typedef float f16v __attribute__((ext_vector_type(16)));
+
+// 16 keys of one page: their scales, as the softmax takes them.
+struct alignas(16) Group {
+    float ks, vs, lg_vs;  // staged: vs is 1 / the value scale, lg_vs its logarithm
+    int on;               // bit 0: some row sees them, bit 1: the value scale is not finite
+};
+
+// Many query rows: 32 rows of one cache head a wave, 64 keys a step.  A step's keys and values are brought to float16 once for all
+// rows and staged in two LDS buffers, the next step's 8-bit values on their
+// way to registers meanwhile.  The products are the same transposed ones on
+// v_mfma_f32_32x32x16_f16 (lane 32 g + n holds A[n][8g..8g+7],
+// B[8g..8g+7][n], and D[8 (r / 4) + 4 g + r % 4][n] in register r): a query
+// row is a column and its probabilities are the next product's operand in
+// the key order 16 u + 8 (j / 4) + 4 g + j % 4, in which V is staged too.
+//
+// LDS: keys as rows of dims, values as rows of keys (transposed on the way
+// in: dim d in row d % 4 * (D / 4) + d / 4, so that a wave writes neighbouring
+// rows and a lane ends with neighbouring dims).  Rows are 16 bytes longer
+// than their contents: 16 of them at one column lie over all the banks.
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_kernel(AttnQ8 a, CacheQ8 c, Ragged r,
+                                                           int splits, int chunk, int tiles,
+                                                           float* part) {
+    constexpr bool kSplit = sizeof(T) == 4;
+    static_assert(kWaves == 4, "a wave for each 16 tokens of a step");
+    constexpr int HEIGHT = 32 * kWaves;
+    constexpr int HS = kSplit || D > 128 ? 1 : 2;  // halves of a step whose scores are held
+    constexpr int KC = D / 16;   // key operands of 16 dims
+    constexpr int DT = D / 32;   // output tiles of 32 dims
+    constexpr int KLD = D + 8, VLD = 64 + 8;  // row lengths
+    __shared__ __align__(16) _Float16 s_k[2][64 * KLD];
+    __shared__ __align__(16) _Float16 s_v[2][D * VLD];
+    __shared__ Group s_group[2 + 16][4];  // two buffers, and room for writes that do not count
+    const int lane = threadIdx.x & 63, wave = wave_id(), n32 = lane & 31, g = lane >> 5;
+    // The longest tiles of all sequences and heads first: with causal rows
+    // these are the last ones.
+    const int pairs = c.heads * r.seqs, pair = blockIdx.x % pairs;
+    const int head = pair % c.heads, b = pair / c.heads;
+    const int split = blockIdx.x / pairs % splits, tile = tiles - 1 - blockIdx.x / pairs / splits;
+    int cu0, n, len;
+    if (!ragged_rows(r, b, cu0, n, len)) {
+        if (cu0 < 0 || n <= 0 || cu0 + (long long)n > r.total) return;
+        len = 0;
+    }
+    const int group = a.q_heads / c.heads, rows = n * group, r0 = tile * HEIGHT;
+    if (r0 >= rows) return;
+    // keys that any of the workgroup's rows sees; bounds grow with the row
+    const Row row0 = row_of(a, c, b, head, cu0, n, len, r0);
+    const Row row1 = row_of(a, c, b, head, cu0, n, len, min(r0 + HEIGHT - 1, rows - 1));
+    const int first = a.first ? max(a.first[b], 0) : 0;
+    const int pos0 = len - n + r0 / group;
+    const int any_lo = a.window ? max(first, pos0 - a.window + 1) : first, any_hi = row1.hi;
+    const int base = any_lo < any_hi ? any_lo & ~63 : 0;
+    const int t_lo = base + split * chunk;
+    const int t_hi = any_lo < any_hi ? min(t_lo + chunk, any_hi) : 0;
+    // keys that this wave's rows see
+    const int w0 = min(r0 + 32 * wave, rows - 1), w1 = min(r0 + 32 * wave + 31, rows - 1);
+    const Row wrow0 = row_of(a, c, b, head, cu0, n, len, w0);
+    const Row wrow1 = row_of(a, c, b, head, cu0, n, len, w1);
+    const bool idle = r0 + 32 * wave >= rows;
+    const Row row = row_of(a, c, b, head, cu0, n, len, r0 + 32 * wave + n32);
+
+    h8 qh[KC], ql[kSplit ? KC : 1];
+    float to_log2;  // not negative: the scale's sign goes into the rows
+    {
+        const T* q = (const T*)a.q + (long long)row.tok * a.q_tok + (long long)row.q_head * a.q_head;
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf((float)q[16 * j + 8 * g + i]));
+        top = max_halves(top);
+        const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 120);
+        const float up = copysignf(__uint_as_float((unsigned)(127 + 14 - e) << 23), a.scale);
+        to_log2 = __uint_as_float((unsigned)(127 - 14 + e) << 23) * fabsf(a.scale) * kLog2e;
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float v = (float)q[16 * j + 8 * g + i] * up;
+                const _Float16 h = (_Float16)v;
+                qh[j][i] = h;
+                if (kSplit) ql[j][i] = (_Float16)(v - (float)h);
+            }
+    }
+
+    // Staging: a wave brings 16 of a step's tokens, which lie in one page, so
+    // that its addresses are a scalar and a lane's constant; the table entry
+    // is read a step ahead of its use.
+    constexpr int KJ = D / 64, VJ = (D + 127) / 128;  // pieces a lane
+    int entry = 0;
+    auto look_up = [&](int t0) { entry = page_entry(c, b, (t0 + 16 * wave) >> c.shift); };
+    Words<4> kw[KJ];
+    unsigned vw[VJ][8];
+    Group next{};
+    auto fetch = [&](int t0) {
+        const int k0 = t0 + 16 * wave;
+        const int page = page_checked(c, k0 >> c.shift, __builtin_amdgcn_readfirstlane(entry));
+        const long long at = (long long)max(page, 0) * c.heads + head;
+        const long long from = (at * c.page + (k0 & (c.page - 1))) * D;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) kw[j] = load_words<4>(c.k + from + (lane + 64 * j) * 16);
+#pragma unroll
+        for (int j = 0; j < VJ; ++j) {
+            const int i = (lane + 64 * j) % (D / 2);
+            const int8_t* v = c.v + from + i / (D / 4) * 4 * D + i % (D / 4) * 4;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                vw[j][k] = load_words<1>(v + ((k & 3) + 8 * (k >> 2)) * D).w[0];
+        }
+        // a group that no row sees may lie in a page that holds anything
+        next.on = page >= 0 && k0 < any_hi && k0 + 16 > any_lo;
+        next.ks = c.k_scale[at];
+        next.vs = c.v_scale[at];
+    };
+    auto stage = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+            const int i = lane + 64 * j;
+            h8* to = reinterpret_cast<h8*>(s_k[buf] + (16 * wave + i / (D / 16)) * KLD +
+                                           i % (D / 16) * 16);
+            to[0] = to_half8(kw[j].w[0], kw[j].w[1]);
+            to[1] = to_half8(kw[j].w[2], kw[j].w[3]);
+        }
+#pragma unroll
+        for (int j = 0; j < VJ; ++j) {
+            const int i = (lane + 64 * j) % (D / 2);  // 64 dims: two lanes do the same
+            unsigned lo01[4], hi01[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                lo01[k] = pair_lo(vw[j][2 * k], vw[j][2 * k + 1]);
+                hi01[k] = pair_hi(vw[j][2 * k], vw[j][2 * k + 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                h2 x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[k] = to_half2(e < 2 ? lo01[k] : hi01[k],
+                                    (e & 1) ? 0x04030402u : 0x04010400u);
+                *reinterpret_cast<h8*>(s_v[buf] + (e * (D / 4) + i % (D / 4)) * VLD +
+                                       (2 * wave + i / (D / 4)) * 8) =
+                    __builtin_bit_cast(h8, x);
+            }
+        }
+        Group to = next;
+        to.ks = to.on ? to.ks : 0.0f;
+        to.vs = to.on ? to.vs : 0.0f;
+        to.on |= finite(to.vs) ? 0 : 2;
+        to.lg_vs = finite(to.vs) ? __builtin_amdgcn_logf(to.vs) : neg_inf();
+        to.vs = __builtin_amdgcn_rcpf(to.vs);
+        // one lane's write counts; the others go aside, so that no branch
+        // parts the step
+        s_group[lane == 0 ? buf : 2 + (lane >> 2)][lane == 0 ? wave : lane & 3] = to;
+    };
+
+    f16v acc[DT] = {};
+    float m = neg_inf(), l = 0.0f;
+    // The accumulated values are in units of 2^(lg_run - 15), lg_run the
+    // largest logarithm of a value scale so far (below every one at first).
+    float lg_run = -140.0f;
+
+    // Scores of 32 HS keys; the halves in turn, so that a product does not
+    // wait for the one before it.
+    auto scores = [&](f16v(&s)[HS], const _Float16* kp) {
+#pragma unroll
+        for (int h = 0; h < HS; ++h) s[h] = (f16v){};
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+#pragma unroll
+            for (int h = 0; h < HS; ++h) {
+                const h8 kv = *reinterpret_cast<const h8*>(kp + 32 * h * KLD + 16 * j);
+                s[h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv, qh[j], s[h], 0, 0, 0);
+                if (kSplit) s[h] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv, ql[j], s[h], 0, 0, 0);
+            }
+    };
+    auto largest = [&](const f16v& s, float by0, float by1) {
+        float top[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            top[u] = s[8 * u];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top[u] = fmaxf(top[u], s[8 * u + j]);
+        }
+        return fmaxf(top[0] * by0, top[1] * by1);
+    };
+    // The rows' references: the largest score and value scale so far, moved
+    // only when a key passes them by so much that p * vs would leave float16
+    // (2^15 at the reference, 2^0.99 above it still fits).
+    auto refer = [&](float top, float lg_vs) {
+        const float m_new = fmaxf(m, max_halves(top));
+        const float lg_new = fmaxf(lg_run, lg_vs);
+        if (__any(m_new - m + (lg_new - lg_run) > 0.99f)) {
+            const float m_at = m_new == neg_inf() ? 0.0f : m_new;
+            const float back = __builtin_amdgcn_exp2f(m - m_at);
+            l *= back;
+            const float to = back * __builtin_amdgcn_exp2f(lg_run - lg_new);
+#pragma unroll
+            for (int t = 0; t < DT; ++t) acc[t] *= to;
+            m = m_new;
+            lg_run = lg_new;
+        }
+    };
+    // Probabilities of 16 keys times their value scale, in the accumulators'
+    // units and straight from the exponent; the sum of the probabilities is
+    // theirs over the same factor.
+    auto weigh = [&](const f16v& s, int u, float by, const Group& gr, h8& ph, h8& pl) {
+        const float m_at = m == neg_inf() ? 0.0f : m;
+        const float lift = fmaxf(gr.lg_vs + 15.0f - lg_run, -60.0f) - m_at;
+        const float drop = fminf(gr.vs * __builtin_amdgcn_exp2f(lg_run - 15.0f), 0x1p60f);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float x0 = __builtin_amdgcn_exp2f(fmaf(s[8 * u + j], by, lift));
+            const float x1 = __builtin_amdgcn_exp2f(fmaf(s[8 * u + j + 1], by, lift));
+            sum += x0 + x1;
+            const h2 hx = __builtin_convertvector(((f2){x0, x1}), h2);
+            ph[j] = hx[0];
+            ph[j + 1] = hx[1];
+            if (kSplit) {
+                pl[j] = (_Float16)(x0 - (float)hx[0]);
+                pl[j + 1] = (_Float16)(x1 - (float)hx[1]);
+            }
+        }
+        l = fmaf(sum, drop, l);
+    };
+    auto add_values = [&](const _Float16* vp, const h8& ph, const h8& pl) {
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+            const h8 vv = *reinterpret_cast<const h8*>(vp + 32 * t * VLD);
+            acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, ph, acc[t], 0, 0, 0);
+            if (kSplit) acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, pl, acc[t], 0, 0, 0);
+        }
+    };
+
+    if (t_lo < t_hi) {
+        look_up(t_lo);
+        fetch(t_lo);
+        look_up(t_lo + 64);
+        stage(0);
+        fetch(t_lo + 64);
+        look_up(t_lo + 128);
+        __syncthreads();
+        for (int t0 = t_lo, buf = 0; t0 < t_hi; t0 += 64, buf ^= 1) {
+            const _Float16* kp = s_k[buf] + n32 * KLD + 8 * g;
+            const _Float16* vp = s_v[buf] + n32 * VLD + 8 * g;
+            const Group* gp = s_group[buf];
+            int seen = t0 >= wrow1.lo && t0 + 64 <= wrow0.hi;  // every row sees every key
+#pragma unroll
+            for (int u = 0; u < 4; ++u) seen &= gp[u].on == 1;
+            seen = __builtin_amdgcn_readfirstlane(seen);
+            // this wave's rows may see none of the step's keys
+            const bool some = !idle && t0 < wrow1.hi && t0 + 64 > wrow0.lo;
+            // (what is staged past the last step is of no use, and harmless)
+            if (!some) {
+                stage(buf ^ 1);
+                fetch(t0 + 128);
+            }
+            if (some)
+#pragma unroll
+                for (int h0 = 0; h0 < 2; h0 += HS) {
+                    f16v s[HS];
+                    float by[2 * HS], top = neg_inf(), lg = neg_inf();
+                    scores(s, kp + 32 * h0 * KLD);
+#pragma unroll
+                    for (int h = 0; h < HS; ++h) {
+                        by[2 * h] = gp[2 * (h0 + h)].ks * to_log2;
+                        by[2 * h + 1] = gp[2 * (h0 + h) + 1].ks * to_log2;
+                    }
+                    if (h0 == 0) {
+                        stage(buf ^ 1);
+                        fetch(t0 + 128);  // a step's time to arrive
+                    }
+                    if (!seen) {
+                        // What is hidden from a row goes into its scores, and
+                        // a value scale that is not finite too: so it stays
+                        // with the rows that see it.
+#pragma unroll
+                        for (int h = 0; h < HS; ++h) {
+                            const int t = t0 + 32 * (h0 + h) + 4 * g;
+                            const int lo = row.lo - t, hi = row.hi - t;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const int at = 8 * (j >> 2) + (j & 3);
+                                const int on = gp[2 * (h0 + h) + j / 8].on;
+                                const float x = on & 2 ? nan() : s[h][j] * by[2 * h + j / 8];
+                                s[h][j] = on & 1 && at >= lo && at < hi ? x : neg_inf();
+                            }
+                            by[2 * h] = by[2 * h + 1] = 1.0f;
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < HS; ++h) {
+                        top = fmaxf(top, largest(s[h], by[2 * h], by[2 * h + 1]));
+                        lg = fmaxf(lg, fmaxf(gp[2 * (h0 + h)].lg_vs, gp[2 * (h0 + h) + 1].lg_vs));
+                    }
+                    refer(top, lg);
+#pragma unroll
+                    for (int u = 0; u < 2 * HS; ++u) {
+                        h8 ph, pl;
+                        weigh(s[u / 2], u & 1, by[u], gp[2 * h0 + u], ph, pl);
+                        add_values(vp + 32 * h0 + 16 * u, ph, pl);
+                    }
+                }
+            look_up(t0 + 192);
+            __syncthreads();
+        }
+    }
+
+    l += __shfl_xor(l, 32);
+    if (!row.live) return;
+    const long long out_row = (long long)row.tok * a.q_heads + row.q_head;
+    const float unit = __builtin_amdgcn_exp2f(lg_run - 15.0f);
+    const float by = splits > 1 ? unit : l == 0.0f ? 0.0f : unit / l;  // a NaN sum stays NaN
+    float* pr = part + (out_row * splits + split) * (D + 4);
+    // dims 4 p .. 4 p + 3 are in rows p, D / 4 + p, D / 2 + p, 3 D / 4 + p of
+    // the stacked output tiles
+#pragma unroll
+    for (int p8 = 0; p8 < D / 4; p8 += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int at = e * (D / 4) + p8;
+                o[e] = acc[at / 32][at % 32 / 8 * 4 + i] * by;
+            }
+            const int d = 4 * (p8 + 4 * g + i);
+            if (splits > 1) {
+                *reinterpret_cast<f4*>(pr + 4 + d) = o;
+            } else {
+                Pack<T, 4> y;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y.v[j] = round_to<T>(o[j]);
+                *reinterpret_cast<Pack<T, 4>*>((T*)a.out + out_row * D + d) = y;
+            }
+        }
+    if (g == 0) {
+        if (splits > 1) {
+            pr[0] = m;
+            pr[1] = l;
+        } else if (a.lse) {
+            a.lse[out_row] = lse_of(m, l);
+        }
+    }
+}
+
 // Joins the chunks of one output row: a thread for four dims, the chunks
 // dealt to the workgroup's lanes beyond them.
 template <typename T, int D>
@@ -400,26 +779,30 @@ __global__ __launch_bounds__(256) void attn_q8_join_kernel(AttnQ8 a, int splits,
     if (a.lse && col == 0) a.lse[row] = lse_of(top, sum);
 }
 
-// How the keys of a row tile are cut: about kChunks pieces in all, each of at
-// least 32 keys a wave.  The lengths are on the device, so this goes by the
-// longest; pieces past a sequence's end are empty.
+// How the rows are tiled and the keys of a tile cut: about kChunks pieces in
+// all, of at least a step each.  The lengths are on the device, so this goes
+// by the longest; pieces past a sequence's end are empty.
 struct Cut {
+    bool many;  // the kernel for many rows
     int tiles, splits, chunk;
 };
 
-constexpr int kChunks = 4096;
-
 Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int window) {
     const int group = q_heads / heads;
+    const long long rows = (long long)max_rows * group;
     Cut r;
-    r.tiles = (int)(((long long)max_rows * group + 15) / 16);
-    long long span = max_len;  // keys of one row tile
-    if (window > 0) span = std::min<long long>(span, (long long)window + 16 / group + 33);
+    r.many = rows > 32;
+    const int height = r.many ? 32 * kWaves : 16;
+    const int step = r.many ? 64 : 32 * kWaves;
+    const int pieces = r.many ? 768 : 4096;
+    r.tiles = (int)((rows + height - 1) / height);
+    long long span = max_len;  // keys of one row tile, from an aligned start
+    if (window > 0) span = std::min<long long>(span, (long long)window + height / group + 65);
     const long long all = span * seqs * heads * r.tiles;
-    const long long step = 32 * kWaves;
-    long long chunk = (all / kChunks + step - 1) / step * step;
-    chunk = std::min(std::max(chunk, step), (span + step - 1) / step * step);
-    r.chunk = (int)std::max(chunk, step);
+    long long chunk = (all / pieces + step - 1) / step * step;
+    if (r.many) chunk = std::max<long long>(chunk, 512);
+    chunk = std::min(std::max<long long>(chunk, step), (span + step - 1) / step * step);
+    r.chunk = (int)std::max<long long>(chunk, step);
     r.splits = (int)std::max<long long>(1, (span + r.chunk - 1) / r.chunk);
     return r;
 }
@@ -428,8 +811,14 @@ template <typename T, int D>
 hipError_t run(const AttnQ8& a, const CacheQ8& c, const Ragged& r, float* part,
                hipStream_t stream) {
     const Cut k = cut(r.seqs, r.max_rows, a.max_len, a.q_heads, c.heads, a.window);
-    hipLaunchKernelGGL((attn_q8_few_kernel<T, D>), dim3(k.tiles * k.splits, c.heads, r.seqs),
-                       dim3(64 * kWaves), 0, stream, a, c, r, k.splits, k.chunk, part);
+    if (k.many)
+        hipLaunchKernelGGL((attn_q8_many_kernel<T, D>),
+                           dim3((unsigned)(k.tiles * k.splits * c.heads * r.seqs)),
+                           dim3(64 * kWaves), 0, stream, a, c, r, k.splits, k.chunk, k.tiles, part);
+    else
+        hipLaunchKernelGGL((attn_q8_few_kernel<T, D>),
+                           dim3((unsigned)(k.tiles * k.splits), c.heads, r.seqs),
+                           dim3(64 * kWaves), 0, stream, a, c, r, k.splits, k.chunk, part);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && k.splits > 1) {
         hipLaunchKernelGGL((attn_q8_join_kernel<T, D>), dim3((unsigned)(r.total * a.q_heads)),

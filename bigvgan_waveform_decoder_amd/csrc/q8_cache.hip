@@ -28,7 +28,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_q8_kernel(
     int cu0, n, len;
     if (!ragged_rows(r, b, cu0, n, len)) return;
     const int start = len - n;  // a start below 0 leaves the first tokens out
-    const int col = max(start, 0) / c.page + blockIdx.x;
+    const int col = (max(start, 0) >> c.shift) + blockIdx.x;
     if ((long long)col * c.page >= len) return;
     const int page = page_of(c, b, col);
     if (page < 0) return;
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_q8_kernel(CacheQ8 c, Ragged 
     const int i = blockIdx.x;  // the i-th of the sequence's last n tokens
     if (!ragged_rows(r, b, cu0, n, len) || i >= n) return;
     const int pos = len - n + i;
-    const int col = pos / c.page;
+    const int col = pos >> c.shift;
     const int page = pos >= 0 ? page_of(c, b, col) : -1;
     const bool there = page >= 0;
     const int row = c.heads * c.dim;

@@ -99,7 +99,7 @@ template <typename T, bool SILU, bool AL, int MT, int NT>
 __global__ __launch_bounds__(512) void linear_q8_rows_kernel(LinearQ8 p) {
     static_assert(MT * NT <= 8, "a wave for each pair of tiles, 8 waves at most");
     __shared__ v4i s_sum[8 * MT * NT * 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id(), waves = blockDim.x >> 6;
     const int i = lane & 15, g = lane >> 4;
     const int n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
     const int8_t* wr[NT];
@@ -201,7 +201,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void linear_q8_tile_kernel(LinearQ8 
     constexpr int PART = (BM + BN) * 128, STEP = KS * 128;
     __shared__ __align__(16) int8_t s_even[KS * PART];
     __shared__ __align__(16) int8_t s_odd[KS * PART];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = wave_id();
     const int i = lane & 15, g = lane >> 4;
 
     // `group` row tiles sweep all column tiles together: what they stage

@@ -591,3 +591,21 @@ def test_attention_pages_next_to_the_seen_keys_may_hold_anything():
         c.table[0, 8] = c.spare[0]  # past the first sequence's length
         for dtype in ("f32", "bf16"):
             _check_attention(c, new, 2, dtype, 3, first=np.array([112, 304], np.int32))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("new,lens,heads,kv_heads,dim,page,window", [
+    ([200], [200], 1, 1, 64, 16, 0), ([129, 40], [700, 40], 3, 1, 128, 64, 0),
+    ([300, 1, 0, 77], [300, 600, 0, 1100], 4, 2, 128, 32, 0), ([100], [1500], 8, 2, 64, 128, 0),
+    ([64], [3000], 4, 2, 128, 16, 0), ([150], [900], 2, 1, 256, 16, 0), ([260], [1300], 2, 2, 64, 32, 70),
+    ([33], [2000], 4, 1, 128, 256, 900), ([130], [100], 2, 2, 64, 16, 0)])
+def test_attention_many_rows(new, lens, heads, kv_heads, dim, page, window, dtype):
+    """Prompts and long drafts: rows over several workgroups, keys split and not."""
+    announce(f"attn_q8 many {new} {lens} {heads}/{kv_heads} dim {dim} page {page} window {window} {dtype}")
+    c = Cache(41, lens, kv_heads, dim, page)
+    c.poison_unused()
+    _check_attention(c, new, heads, dtype, 10, window=window)
+    first = np.array([17 + 300 * (t > 1000) for t in lens], np.int32)
+    _check_attention(c, new, heads, dtype, 11, window=window, first=first)
+    if not window:
+        _check_attention(c, new, heads, dtype, 12, causal=False, first=first)
