@@ -874,117 +874,161 @@ class BweDecoder:
 
 
 # ------------------------------------------------------------------ 8-bit serving operators
+#
+# These calls take a few microseconds on the device, so what the binding does
+# for each of them counts: names are looked up once, and a tensor is asked
+# for its properties once.
 
 ACT = {"none": 0, "silu": 1}
-_DTYPES: Dict = {}
 
 
-def _dtype_code(dtype) -> int:
-    if not _DTYPES:
+class _Env:
+    """torch, the library's functions and the types, looked up once."""
+
+    def __init__(self):
         torch = _torch()
-        _DTYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    try:
-        return _DTYPES[dtype]
-    except KeyError:
-        raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}") from None
+        L = lib()
+        self.empty = torch.empty
+        self.int8, self.int32, self.uint8 = torch.int8, torch.int32, torch.uint8
+        self.float32 = torch.float32
+        self.codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.norm, self.quant, self.dequant = (L.avae_rms_norm_q8, L.avae_quant_q8,
+                                               L.avae_dequant_q8)
+        self.linear, self.linear_ws = L.avae_linear_q8, L.avae_linear_q8_workspace_bytes
+        self.write, self.read = L.avae_kv_write_q8, L.avae_kv_read_q8
+        self.attn, self.attn_ws = L.avae_attn_q8, L.avae_attn_q8_workspace_bytes
+
+    def code(self, dtype) -> int:
+        code = self.codes.get(dtype)
+        if code is None:
+            raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+        return code
+
+    def stream(self, t, stream):
+        """The raw stream to launch on: the given one, or the current one of
+        the tensor's device."""
+        return self.raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
-def _rows(t, name: str, dtype, cols: Optional[int] = None, rows: Optional[int] = None):
-    """Pointer and row stride of a [rows, cols] device tensor whose last axis
-    is contiguous."""
+_env: Optional[_Env] = None
+
+
+def _q8() -> _Env:
+    global _env
+    if _env is None:
+        _env = _Env()
+    return _env
+
+
+def _bad(t, name: str, dtype, expected: str):
+    """Says what is wrong with a tensor that a check refused."""
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name}: must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected two axes, got {tuple(t.shape)}")
-    m, n = t.shape
-    if (cols is not None and n != cols) or (rows is not None and m != rows):
-        raise ValueError(f"{name}: expected shape ({rows}, {cols}), got {(m, n)}")
+    raise ValueError(f"{name}: expected {expected} with the last axis contiguous, got "
+                     f"{tuple(t.shape)} at strides {t.stride()}")
+
+
+def _rows(t, name: str, dtype, rows: int, cols: int):
+    """Pointer and row stride of a [rows, cols] device tensor whose last axis
+    is contiguous."""
+    if not t.is_cuda or t.dtype != dtype or t.shape != (rows, cols):
+        _bad(t, name, dtype, f"[{rows}, {cols}]")
     ld, one = t.stride()
-    if one != 1 and n > 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
+    if one != 1 and cols > 1:
+        _bad(t, name, dtype, f"[{rows}, {cols}]")
     # the stride of a single row says nothing; torch may give any
-    return t.data_ptr(), (ld if m > 1 else max(ld, n))
+    return t.data_ptr(), (ld if rows > 1 else cols)
 
 
 def _vec(t, name: str, n: int, dtype):
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a device tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: must be {dtype}, got {t.dtype}")
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous vector of {n}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
+        _bad(t, name, dtype, f"[{n}]")
     return t.data_ptr()
+
+
+def _two_axes(t, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected two axes, got {tuple(t.shape)}")
+    return t.shape
 
 
 def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, stream=None):
     """avae_rms_norm_q8: x [M, C] (+ residual) -> (q [M, C] int8, scale [M],
     the sum in x's dtype or None)."""
-    torch = _torch()
-    M, C = x.shape
-    dt = _dtype_code(x.dtype)
-    px, ldx = _rows(x, "x", x.dtype)
-    dev = x.device
-    q = torch.empty((M, C), dtype=torch.int8, device=dev)
-    scale = torch.empty((M,), dtype=torch.float32, device=dev)
+    E = _q8()
+    M, C = _two_axes(x, "x")
+    dtype, dev = x.dtype, x.device
+    code = E.code(dtype)
+    px, ldx = _rows(x, "x", dtype, M, C)
+    q = E.empty((M, C), dtype=E.int8, device=dev)
+    scale = E.empty((M,), dtype=E.float32, device=dev)
     pr, ldr, total, pt = None, 0, None, None
     if residual is not None:
-        pr, ldr = _rows(residual, "residual", x.dtype, C, M)
-        total = torch.empty((M, C), dtype=x.dtype, device=dev)
+        pr, ldr = _rows(residual, "residual", dtype, M, C)
+        total = E.empty((M, C), dtype=dtype, device=dev)
         pt = total.data_ptr()
-    _check(lib().avae_rms_norm_q8(px, ldx, pr, ldr, _vec(weight, "weight", C, torch.float32), M, C,
-                                  dt, eps, pt, C, q.data_ptr(), C, scale.data_ptr(),
-                                  _stream(stream)))
+    rc = E.norm(px, ldx, pr, ldr, _vec(weight, "weight", C, E.float32), M, C, code, eps, pt, C,
+                q.data_ptr(), C, scale.data_ptr(), E.stream(x, stream))
+    if rc:
+        _check(rc)
     return q, scale, total
 
 
 def quant_q8(x, stream=None):
     """avae_quant_q8: x [M, C] -> (q [M, C] int8, scale [M])."""
-    torch = _torch()
-    M, C = x.shape
-    dt = _dtype_code(x.dtype)
-    px, ldx = _rows(x, "x", x.dtype)
-    q = torch.empty((M, C), dtype=torch.int8, device=x.device)
-    scale = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _check(lib().avae_quant_q8(px, ldx, M, C, dt, q.data_ptr(), C, scale.data_ptr(),
-                               _stream(stream)))
+    E = _q8()
+    M, C = _two_axes(x, "x")
+    code = E.code(x.dtype)
+    px, ldx = _rows(x, "x", x.dtype, M, C)
+    q = E.empty((M, C), dtype=E.int8, device=x.device)
+    scale = E.empty((M,), dtype=E.float32, device=x.device)
+    rc = E.quant(px, ldx, M, C, code, q.data_ptr(), C, scale.data_ptr(), E.stream(x, stream))
+    if rc:
+        _check(rc)
     return q, scale
 
 
 def dequant_q8(q, scale, dtype=None, stream=None):
     """avae_dequant_q8: q [M, C] int8 with a scale a row -> [M, C] of dtype
     (float32 if none is given)."""
-    torch = _torch()
-    dtype = torch.float32 if dtype is None else dtype
-    M, C = q.shape
-    pq, ldq = _rows(q, "q", torch.int8)
-    y = torch.empty((M, C), dtype=dtype, device=q.device)
-    _check(lib().avae_dequant_q8(pq, ldq, _vec(scale, "scale", M, torch.float32), M, C,
-                                 _dtype_code(dtype), y.data_ptr(), C, _stream(stream)))
+    E = _q8()
+    dtype = E.float32 if dtype is None else dtype
+    M, C = _two_axes(q, "q")
+    code = E.code(dtype)
+    pq, ldq = _rows(q, "q", E.int8, M, C)
+    y = E.empty((M, C), dtype=dtype, device=q.device)
+    rc = E.dequant(pq, ldq, _vec(scale, "scale", M, E.float32), M, C, code, y.data_ptr(), C,
+                   E.stream(q, stream))
+    if rc:
+        _check(rc)
     return y
 
 
 def linear_q8(a, a_scale, w, w_scale, bias=None, act: str = "none", dtype=None, stream=None):
     """avae_linear_q8: a [M, K] int8, w [N, K] int8 with a scale a row each
     -> [M, N] of dtype (float32 if none is given)."""
-    torch = _torch()
-    dtype = torch.float32 if dtype is None else dtype
-    M, K = a.shape
-    N = w.shape[0]
-    pa, lda = _rows(a, "a", torch.int8)
-    pw, ldw = _rows(w, "w", torch.int8, K)
-    if act not in ACT:
+    E = _q8()
+    dtype = E.float32 if dtype is None else dtype
+    M, K = _two_axes(a, "a")
+    N = _two_axes(w, "w")[0]
+    code, act_code = E.code(dtype), ACT.get(act)
+    if act_code is None:
         raise ValueError(f"act must be one of {sorted(ACT)}, got {act!r}")
-    y = torch.empty((M, N), dtype=dtype, device=a.device)
-    L = lib()
-    need = L.avae_linear_q8_workspace_bytes(M, N, K)
-    ws = torch.empty((need,), dtype=torch.uint8, device=a.device) if need else None
-    _check(L.avae_linear_q8(pa, lda, _vec(a_scale, "a_scale", M, torch.float32), pw, ldw,
-                            _vec(w_scale, "w_scale", N, torch.float32),
-                            None if bias is None else _vec(bias, "bias", N, torch.float32),
-                            M, N, K, ACT[act], _dtype_code(dtype), y.data_ptr(), N,
-                            None if ws is None else ws.data_ptr(), need, _stream(stream)))
+    pa, lda = _rows(a, "a", E.int8, M, K)
+    pw, ldw = _rows(w, "w", E.int8, N, K)
+    y = E.empty((M, N), dtype=dtype, device=a.device)
+    need = E.linear_ws(M, N, K)
+    ws = E.empty((need,), dtype=E.uint8, device=a.device) if need else None
+    rc = E.linear(pa, lda, _vec(a_scale, "a_scale", M, E.float32), pw, ldw,
+                  _vec(w_scale, "w_scale", N, E.float32),
+                  None if bias is None else _vec(bias, "bias", N, E.float32), M, N, K, act_code,
+                  code, y.data_ptr(), N, None if ws is None else ws.data_ptr(), need,
+                  E.stream(a, stream))
+    if rc:
+        _check(rc)
     return y
 
 
@@ -992,24 +1036,24 @@ class KvCacheQ8:
     """The four tensors of a paged 8-bit cache (avae_kv_q8): k, v [n_pages,
     heads, page, dim] int8 and k_scale, v_scale [n_pages, heads] float32."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "c")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "heads", "page", "dim", "c", "ref")
 
     def __init__(self, k, v, k_scale, v_scale):
-        torch = _torch()
-        for name, t, dtype, shape in (("k", k, torch.int8, k.shape), ("v", v, torch.int8, k.shape),
-                                      ("k_scale", k_scale, torch.float32, k.shape[:2]),
-                                      ("v_scale", v_scale, torch.float32, k.shape[:2])):
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{name}: must be a contiguous device tensor")
-            if t.dtype != dtype:
-                raise ValueError(f"{name}: must be {dtype}, got {t.dtype}")
-            if t.shape != shape:
-                raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        E = _q8()
         if k.dim() != 4:
             raise ValueError(f"k: expected [n_pages, heads, page, dim], got {tuple(k.shape)}")
+        shape = k.shape
+        scales = shape[:2]
+        for name, t, dtype, want in (("k", k, E.int8, shape), ("v", v, E.int8, shape),
+                                     ("k_scale", k_scale, E.float32, scales),
+                                     ("v_scale", v_scale, E.float32, scales)):
+            if not t.is_cuda or t.dtype != dtype or t.shape != want or not t.is_contiguous():
+                _bad(t, name, dtype, f"{tuple(want)}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        _, self.heads, self.page, self.dim = shape
         self.c = avae_kv_q8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                            *k.shape)
+                            *shape)
+        self.ref = ctypes.addressof(self.c)
 
     @classmethod
     def empty(cls, n_pages: int, heads: int, page: int, dim: int, device="cuda"):
@@ -1021,26 +1065,22 @@ class KvCacheQ8:
                    *(torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
 
 
-def _ragged(table, cu, lens, total: int, max_rows: int):
-    i32 = _torch().int32
-    if table.dim() != 2:
-        raise ValueError(f"table: expected [sequences, pages], got {tuple(table.shape)}")
-    seqs, cols = table.shape
-    pt, ld = _rows(table, "table", i32)
-    return avae_ragged(_vec(cu, "cu", seqs + 1, i32), _vec(lens, "lens", seqs, i32), pt, ld, cols,
-                       seqs, total, max_rows)
+def _ragged(E, table, cu, lens, total: int, max_rows: Optional[int]):
+    seqs, cols = _two_axes(table, "table")
+    pt, ld = _rows(table, "table", E.int32, seqs, cols)
+    return avae_ragged(_vec(cu, "cu", seqs + 1, E.int32), _vec(lens, "lens", seqs, E.int32), pt, ld,
+                       cols, seqs, total,
+                       total if max_rows is None or max_rows > total else max_rows)
 
 
 def _heads(t, name: str, heads: Optional[int], dim: int):
     """Pointer, token and head stride of a [tokens, heads, dim] tensor."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a device tensor")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name}: expected [tokens, {heads or 'heads'}, {dim}], "
-                         f"got {tuple(t.shape)}")
+    if (not t.is_cuda or t.dim() != 3 or t.shape[2] != dim
+            or (heads is not None and t.shape[1] != heads)):
+        _bad(t, name, t.dtype, f"[tokens, {heads or 'heads'}, {dim}]")
     tok, head, one = t.stride()
     if one != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
+        _bad(t, name, t.dtype, f"[tokens, {heads or 'heads'}, {dim}]")
     return t.data_ptr(), tok, head
 
 
@@ -1048,28 +1088,32 @@ def kv_write_q8(cache: KvCacheQ8, k, v, table, cu, lens, max_new: Optional[int] 
                 stream=None):
     """avae_kv_write_q8: k, v [tokens, heads, dim] into the cache's pages.
     max_new: at least the most rows of one sequence (all of them if not given)."""
-    c = cache.c
-    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
-        raise ValueError("k and v must have one dtype and as many tokens")
+    E = _q8()
     total = k.shape[0]
-    rows = _ragged(table, cu, lens, total, total if max_new is None else min(max_new, total))
-    _check(lib().avae_kv_write_q8(*_heads(k, "k", c.heads, c.dim), *_heads(v, "v", c.heads, c.dim),
-                                  _dtype_code(k.dtype), ctypes.byref(c), ctypes.byref(rows),
-                                  _stream(stream)))
+    if v.dtype != k.dtype or v.shape[0] != total:
+        raise ValueError("k and v must have one dtype and as many tokens")
+    rows = _ragged(E, table, cu, lens, total, max_new)
+    rc = E.write(*_heads(k, "k", cache.heads, cache.dim), *_heads(v, "v", cache.heads, cache.dim),
+                 E.code(k.dtype), cache.ref, ctypes.addressof(rows), E.stream(k, stream))
+    if rc:
+        _check(rc)
 
 
 def kv_read_q8(cache: KvCacheQ8, table, cu, lens, total: int, max_rows: Optional[int] = None,
                dtype=None, stream=None):
     """avae_kv_read_q8: the sequences' last tokens, `total` of them, as cu
     says -> k, v [total, heads, dim] of dtype (float32 if none is given)."""
-    torch = _torch()
-    c = cache.c
-    dtype = torch.float32 if dtype is None else dtype
-    k, v = (torch.empty((total, c.heads, c.dim), dtype=dtype, device=cache.k.device)
-            for _ in range(2))
-    rows = _ragged(table, cu, lens, total, total if max_rows is None else min(max_rows, total))
-    _check(lib().avae_kv_read_q8(ctypes.byref(c), ctypes.byref(rows), _dtype_code(dtype),
-                                 k.data_ptr(), v.data_ptr(), _stream(stream)))
+    E = _q8()
+    dtype = E.float32 if dtype is None else dtype
+    code = E.code(dtype)
+    shape, dev = (total, cache.heads, cache.dim), cache.k.device
+    k = E.empty(shape, dtype=dtype, device=dev)
+    v = E.empty(shape, dtype=dtype, device=dev)
+    rows = _ragged(E, table, cu, lens, total, max_rows)
+    rc = E.read(cache.ref, ctypes.addressof(rows), code, k.data_ptr(), v.data_ptr(),
+                E.stream(cache.k, stream))
+    if rc:
+        _check(rc)
     return k, v
 
 
@@ -1080,22 +1124,24 @@ def attn_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = None,
     (and lse [tokens, q_heads] float32 if asked for).  max_q: at least the most
     rows of one sequence; max_len: at least the longest sequence (the table's
     tokens if not given); scale: 1 / sqrt(dim) if not given."""
-    torch = _torch()
-    c = cache.c
-    pq, tok, head = _heads(q, "q", None, c.dim)
-    total, heads = q.shape[:2]
-    rows = _ragged(table, cu, lens, total, total if max_q is None else min(max_q, total))
+    E = _q8()
+    dim, dtype, dev = cache.dim, q.dtype, q.device
+    code = E.code(dtype)
+    pq, tok, head = _heads(q, "q", None, dim)
+    total, heads, _ = q.shape
+    rows = _ragged(E, table, cu, lens, total, max_q)
+    pr = ctypes.addressof(rows)
     if max_len is None:
-        max_len = rows.table_cols * c.page
-    out = torch.empty((total, heads, c.dim), dtype=q.dtype, device=q.device)
-    lse = torch.empty((total, heads), dtype=torch.float32, device=q.device) if return_lse else None
-    L = lib()
-    pc, pr = ctypes.byref(c), ctypes.byref(rows)
-    need = L.avae_attn_q8_workspace_bytes(pc, pr, heads, max_len, window)
-    ws = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
-    _check(L.avae_attn_q8(pq, tok, head, heads, _dtype_code(q.dtype), pc, pr,
-                          None if first is None else _vec(first, "first", rows.seqs, torch.int32),
-                          max_len, c.dim ** -0.5 if scale is None else scale, 1 if causal else 0,
-                          window, out.data_ptr(), None if lse is None else lse.data_ptr(),
-                          None if ws is None else ws.data_ptr(), need, _stream(stream)))
+        max_len = rows.table_cols * cache.page
+    out = E.empty((total, heads, dim), dtype=dtype, device=dev)
+    lse = E.empty((total, heads), dtype=E.float32, device=dev) if return_lse else None
+    need = E.attn_ws(cache.ref, pr, heads, max_len, window)
+    ws = E.empty((need,), dtype=E.uint8, device=dev) if need else None
+    rc = E.attn(pq, tok, head, heads, code, cache.ref, pr,
+                None if first is None else _vec(first, "first", rows.seqs, E.int32), max_len,
+                dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+                out.data_ptr(), None if lse is None else lse.data_ptr(),
+                None if ws is None else ws.data_ptr(), need, E.stream(q, stream))
+    if rc:
+        _check(rc)
     return (out, lse) if return_lse else out
