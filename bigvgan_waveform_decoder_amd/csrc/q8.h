@@ -41,10 +41,86 @@ __device__ inline float scale_of(unsigned amax_bits) {
 }
 
 // The stored value nearest x / scale (ties to even, the division correctly
-// rounded).  0 where the scale is 0 or NaN.
-__device__ inline int quantise(float x, float scale) {
-    if (!(scale > 0.0f)) return 0;
-    return (int)fminf(fmaxf(rintf(x / scale), -127.0f), 127.0f);
+// rounded), for |x| <= 127 scale; 0 where the scale is 0 or NaN.  The
+// quotient is x times the reciprocal, corrected by its own remainder (exact
+// in one fmaf); scales so small or large that reciprocal or remainder would
+// leave float32's normal range take the division itself.
+struct Quantiser {
+    float scale, inv;
+    bool plain;
+
+    __device__ explicit Quantiser(float s) : scale(s), inv(1.0f / s), plain(s >= 1e-30f && s <= 1e30f) {}
+
+    __device__ float quotient(float x) const {
+        if (plain) {
+            const float r = x * inv;
+            return fmaf(fmaf(-r, scale, x), inv, r);
+        }
+        return scale > 0.0f ? x / scale : 0.0f;
+    }
+};
+
+// Four quotients in [-127.5, 127.5) rounded to bytes.  Adding 1.5 * 2^23
+// leaves the nearest whole number (ties to even) in the low bits.
+__device__ inline unsigned to_bytes(float a, float b, float c, float d) {
+    constexpr float kRound = 12582912.0f;
+    const unsigned x = __float_as_uint(a + kRound), y = __float_as_uint(b + kRound);
+    const unsigned z = __float_as_uint(c + kRound), w = __float_as_uint(d + kRound);
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(w, z, 0x0c0c0400u),
+                                 __builtin_amdgcn_perm(y, x, 0x0c0c0400u), 0x05040100u);
+}
+
+// N consecutive values from any address; what lies past `left` of them is 0.
+template <int N, typename T>
+__device__ inline void load_values(const T* p, int left, float (&x)[N]) {
+    if (left >= N) {
+        T v[N];
+        __builtin_memcpy(v, p, sizeof(v));
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = (float)v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = i < left ? (float)p[i] : 0.0f;
+    }
+}
+
+template <int N, typename T>
+__device__ inline void store_values(T* p, int left, const float (&x)[N]) {
+    T v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = round_to<T>(x[i]);
+    if (left >= N) {
+        __builtin_memcpy(p, v, sizeof(v));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < left) p[i] = v[i];
+    }
+}
+
+template <int N>
+__device__ inline void store_bytes(int8_t* p, int left, const unsigned (&w)[N / 4]) {
+    if (left >= N) {
+        __builtin_memcpy(p, w, N);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < left) p[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+}
+
+// N stored values from any address as floats.
+template <int N>
+__device__ inline void load_stored(const int8_t* p, int left, float (&x)[N]) {
+    if (left >= N) {
+        int8_t v[N];
+        __builtin_memcpy(v, p, N);
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = (float)v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = i < left ? (float)p[i] : 0.0f;
+    }
 }
 
 // Rows cu[b] .. cu[b+1] of sequence b; false if it has none, or if the

@@ -19,21 +19,96 @@ namespace {
 
 using namespace q8;
 
-constexpr int kThreads = 256;
+// One row a group of THREADS threads (64 of a workgroup of 256, or a whole
+// workgroup of 256 or 1024), its values held in registers between the pass
+// that finds the maximum and the one that rounds: 8 HELD a thread.
+template <typename T, bool RES, bool NORM, int THREADS, int HELD>
+__global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rows_q8_kernel(
+    const T* __restrict__ x, long long ldx, const T* __restrict__ res, long long ldr,
+    const float* __restrict__ w, int M, int C, float eps, T* __restrict__ sum, long long lds,
+    int8_t* __restrict__ q, long long ldq, float* __restrict__ scale) {
+    constexpr int WAVES = THREADS / 64;
+    __shared__ unsigned s_max[WAVES];
+    __shared__ float s_sq[WAVES];
+    const int wave = wave_id();
+    const long long row = THREADS == 64 ? blockIdx.x * 4LL + wave : blockIdx.x;
+    if (row >= M) return;  // whole waves, and only where a wave has a row to itself
+    const int tid = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
+    float v[HELD][8];
+    unsigned top = 0;
+    float sq = 0.0f;
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+        const int c = (tid + j * THREADS) * 8, left = C - c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+        if (left <= 0) continue;
+        load_values<8>(x + row * ldx + c, left, v[j]);
+        if (RES) {
+            float r[8];
+            load_values<8>(res + row * ldr + c, left, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] += r[i];
+            store_values<8>(sum + row * lds + c, left, v[j]);
+        }
+        if (NORM) {
+            float g[8];
+            load_values<8>(w + c, left, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sq += v[j][i] * v[j][i];
+                v[j][i] *= g[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, mag_bits(v[j][i]));
+    }
+    top = wave_max(top);
+    if (NORM) sq = wave_sum(sq);
+    if (WAVES > 1) {
+        if ((threadIdx.x & 63) == 0) {
+            s_max[wave] = top;
+            s_sq[wave] = sq;
+        }
+        __syncthreads();
+        top = 0;
+        sq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            top = max(top, s_max[i]);
+            sq += s_sq[i];
+        }
+    }
+    const float s = scale_of(top);
+    if (tid == 0) scale[row] = NORM ? s * (1.0f / sqrtf(sq / (float)C + eps)) : s;
+    const Quantiser quant(s);
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+        const int c = (tid + j * THREADS) * 8, left = C - c;
+        if (left <= 0) continue;
+        unsigned out[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            out[h] = to_bytes(quant.quotient(v[j][4 * h]), quant.quotient(v[j][4 * h + 1]),
+                              quant.quotient(v[j][4 * h + 2]), quant.quotient(v[j][4 * h + 3]));
+        store_bytes<8>(q + row * ldq + c, left, out);
+    }
+}
 
+// Rows too long for the registers: read twice.
 template <typename T, bool RES, bool NORM>
-__global__ __launch_bounds__(kThreads) void rows_q8_kernel(
+__global__ __launch_bounds__(1024) void long_rows_q8_kernel(
     const T* __restrict__ x, long long ldx, const T* __restrict__ res, long long ldr,
     const float* __restrict__ w, int C, float eps, T* __restrict__ sum, long long lds,
     int8_t* __restrict__ q, long long ldq, float* __restrict__ scale) {
-    __shared__ unsigned s_max[kThreads / 64];
-    __shared__ float s_sq[kThreads / 64];
+    __shared__ unsigned s_max[16];
+    __shared__ float s_sq[16];
     const long long row = blockIdx.x;
     const T* xr = x + row * ldx;
     const T* rr = RES ? res + row * ldr : nullptr;
     unsigned top = 0;
     float sq = 0.0f;
-    for (int c = threadIdx.x; c < C; c += kThreads) {
+    for (int c = threadIdx.x; c < C; c += 1024) {
         float h = (float)xr[c];
         if (RES) {
             h += (float)rr[c];
@@ -51,48 +126,102 @@ __global__ __launch_bounds__(kThreads) void rows_q8_kernel(
     __syncthreads();
     top = 0;
     sq = 0.0f;
-    for (int i = 0; i < kThreads / 64; ++i) {
+    for (int i = 0; i < 16; ++i) {
         top = max(top, s_max[i]);
         sq += s_sq[i];
     }
     const float s = scale_of(top);
     if (threadIdx.x == 0) scale[row] = NORM ? s * (1.0f / sqrtf(sq / (float)C + eps)) : s;
-    for (int c = threadIdx.x; c < C; c += kThreads) {
+    const Quantiser quant(s);
+    for (int c = threadIdx.x; c < C; c += 1024) {
         float h = (float)xr[c];
         if (RES) h += (float)rr[c];
-        q[row * ldq + c] = (int8_t)quantise(NORM ? h * w[c] : h, s);
+        q[row * ldq + c] =
+            (int8_t)to_bytes(quant.quotient(NORM ? h * w[c] : h), 0.0f, 0.0f, 0.0f);
     }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void dequant_q8_kernel(const int8_t* __restrict__ q,
-                                                              long long ldq,
-                                                              const float* __restrict__ scale,
-                                                              int C, T* __restrict__ y,
-                                                              long long ldy) {
-    const long long row = blockIdx.x;
+// Eight values a thread; THREADS of them walk a row.
+template <typename T, int THREADS>
+__global__ __launch_bounds__(256) void dequant_q8_kernel(const int8_t* __restrict__ q,
+                                                         long long ldq,
+                                                         const float* __restrict__ scale, int M,
+                                                         int C, T* __restrict__ y,
+                                                         long long ldy) {
+    const long long row = THREADS == 64 ? blockIdx.x * 4LL + wave_id() : blockIdx.x;
+    if (row >= M) return;
+    const int tid = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
     const float s = scale[row];
-    for (int c = threadIdx.x; c < C; c += kThreads)
-        y[row * ldy + c] = round_to<T>((float)q[row * ldq + c] * s);
+    for (int c = tid * 8; c < C; c += THREADS * 8) {
+        float v[8];
+        load_stored<8>(q + row * ldq + c, C - c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= s;
+        store_values<8>(y + row * ldy + c, C - c, v);
+    }
+}
+
+template <typename T, bool RES, bool NORM>
+hipError_t rows_q8(const void* x, long long ldx, const void* res, long long ldr, const float* w,
+                   int M, int C, float eps, void* sum, long long lds, int8_t* q, long long ldq,
+                   float* scale, hipStream_t stream) {
+    const T* px = (const T*)x;
+    const T* pr = (const T*)res;
+    T* ps = (T*)sum;
+#define AVAE_ROWS(THREADS, HELD)                                                                 \
+    hipLaunchKernelGGL((rows_q8_kernel<T, RES, NORM, THREADS, HELD>),                            \
+                       dim3((unsigned)(THREADS == 64 ? (M + 3LL) / 4 : M)),                      \
+                       dim3(THREADS < 256 ? 256 : THREADS), 0, stream, px, ldx, pr, ldr, w, M, C, \
+                       eps, ps, lds, q, ldq, scale)
+    // A wave for a row where there are rows for all the CUs' waves, else a
+    // workgroup, which has less of the row to wait for.
+    const bool many = M >= 2048;
+    if (C <= 512)
+        AVAE_ROWS(64, 1);
+    else if (many && C <= 1024)
+        AVAE_ROWS(64, 2);
+    else if (many && C <= 2048)
+        AVAE_ROWS(64, 4);
+    else if (C <= 2048)
+        AVAE_ROWS(256, 1);
+    else if (C <= 4096)
+        AVAE_ROWS(256, 2);
+    else if (C <= 8192)
+        AVAE_ROWS(256, 4);
+    else if (C <= 16384)
+        AVAE_ROWS(1024, 2);
+    else if (C <= 32768)
+        AVAE_ROWS(1024, 4);
+    else
+        hipLaunchKernelGGL((long_rows_q8_kernel<T, RES, NORM>), dim3((unsigned)M), dim3(1024), 0,
+                           stream, px, ldx, pr, ldr, w, C, eps, ps, lds, q, ldq, scale);
+#undef AVAE_ROWS
+    return hipGetLastError();
 }
 
 template <typename T>
 hipError_t rows_q8(const void* x, long long ldx, const void* res, long long ldr, const float* w,
                    int M, int C, float eps, void* sum, long long lds, int8_t* q, long long ldq,
                    float* scale, hipStream_t stream) {
-    const dim3 grid((unsigned)M), block(kThreads);
-    const T* px = (const T*)x;
-    const T* pr = (const T*)res;
-    T* ps = (T*)sum;
-    if (res && w)
-        hipLaunchKernelGGL((rows_q8_kernel<T, true, true>), grid, block, 0, stream, px, ldx, pr,
-                           ldr, w, C, eps, ps, lds, q, ldq, scale);
-    else if (w)
-        hipLaunchKernelGGL((rows_q8_kernel<T, false, true>), grid, block, 0, stream, px, ldx, pr,
-                           ldr, w, C, eps, ps, lds, q, ldq, scale);
+    if (res)
+        return rows_q8<T, true, true>(x, ldx, res, ldr, w, M, C, eps, sum, lds, q, ldq, scale,
+                                      stream);
+    if (w)
+        return rows_q8<T, false, true>(x, ldx, res, ldr, w, M, C, eps, sum, lds, q, ldq, scale,
+                                       stream);
+    return rows_q8<T, false, false>(x, ldx, res, ldr, w, M, C, eps, sum, lds, q, ldq, scale,
+                                    stream);
+}
+
+template <typename T>
+hipError_t dequant_q8(const int8_t* q, long long ldq, const float* scale, int M, int C, void* y,
+                      long long ldy, hipStream_t stream) {
+    if (M >= 2048 || C <= 512)
+        hipLaunchKernelGGL((dequant_q8_kernel<T, 64>), dim3((unsigned)((M + 3LL) / 4)), dim3(256),
+                           0, stream, q, ldq, scale, M, C, (T*)y, ldy);
     else
-        hipLaunchKernelGGL((rows_q8_kernel<T, false, false>), grid, block, 0, stream, px, ldx, pr,
-                           ldr, w, C, eps, ps, lds, q, ldq, scale);
+        hipLaunchKernelGGL((dequant_q8_kernel<T, 256>), dim3((unsigned)M), dim3(256), 0, stream, q,
+                           ldq, scale, M, C, (T*)y, ldy);
     return hipGetLastError();
 }
 
@@ -117,17 +246,10 @@ hipError_t launch_rows_q8(int dtype, const void* x, long long ldx, const void* r
 hipError_t launch_dequant_q8(int dtype, const int8_t* q, long long ldq, const float* scale, int M,
                              int C, void* y, long long ldy, hipStream_t stream) {
     prof_pre(stream);
-    const dim3 grid((unsigned)M), block(kThreads);
-    if (dtype == AVAE_F32)
-        hipLaunchKernelGGL(dequant_q8_kernel<float>, grid, block, 0, stream, q, ldq, scale, C,
-                           (float*)y, ldy);
-    else if (dtype == AVAE_BF16)
-        hipLaunchKernelGGL(dequant_q8_kernel<__bf16>, grid, block, 0, stream, q, ldq, scale, C,
-                           (__bf16*)y, ldy);
-    else
-        hipLaunchKernelGGL(dequant_q8_kernel<_Float16>, grid, block, 0, stream, q, ldq, scale, C,
-                           (_Float16*)y, ldy);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e =
+        dtype == AVAE_F32    ? dequant_q8<float>(q, ldq, scale, M, C, y, ldy, stream)
+        : dtype == AVAE_BF16 ? dequant_q8<__bf16>(q, ldq, scale, M, C, y, ldy, stream)
+                             : dequant_q8<_Float16>(q, ldq, scale, M, C, y, ldy, stream);
     const double n = (double)M * C;
     prof_post(stream, "dequant_q8_kernel", n, n * (1 + (dtype == AVAE_F32 ? 4 : 2)));
     return e;
