@@ -220,7 +220,7 @@ def lib() -> ctypes.CDLL:
     L.avae_kv_read_q8.restype = c_int
     L.avae_kv_read_q8.argtypes = [P, P, c_int, P, P, P]
     L.avae_attn_q8_workspace_bytes.restype = c_size_t
-    L.avae_attn_q8_workspace_bytes.argtypes = [P, P, c_int, c_int, c_int]
+    L.avae_attn_q8_workspace_bytes.argtypes = [P, P, c_int, c_int, c_int, c_int]
     L.avae_attn_q8.restype = c_int
     L.avae_attn_q8.argtypes = [P, LL, LL, c_int, c_int, P, P, P, c_int, c_float, c_int, c_int, P,
                                P, P, c_size_t, P]
@@ -1135,7 +1135,7 @@ def attn_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = None,
         max_len = rows.table_cols * cache.page
     out = E.empty((total, heads, dim), dtype=dtype, device=dev)
     lse = E.empty((total, heads), dtype=E.float32, device=dev) if return_lse else None
-    need = E.attn_ws(cache.ref, pr, heads, max_len, window)
+    need = E.attn_ws(cache.ref, pr, heads, code, max_len, window)
     ws = E.empty((need,), dtype=E.uint8, device=dev) if need else None
     rc = E.attn(pq, tok, head, heads, code, cache.ref, pr,
                 None if first is None else _vec(first, "first", rows.seqs, E.int32), max_len,

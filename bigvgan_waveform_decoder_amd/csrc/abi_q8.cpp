@@ -256,12 +256,12 @@ extern "C" int avae_kv_read_q8(const avae_kv_q8* cache, const avae_ragged* rows,
 }
 
 extern "C" size_t avae_attn_q8_workspace_bytes(const avae_kv_q8* cache, const avae_ragged* rows,
-                                               int q_heads, int max_len, int window) {
-    if (!cache || !rows || cache->heads < 1 || cache->dim < 1 || q_heads < 1 || rows->seqs < 1 ||
+                                               int q_heads, int dtype, int max_len, int window) {
+    if (bad_dtype(dtype) || !cache || !rows || cache->heads < 1 || cache->dim < 1 || q_heads < 1 || rows->seqs < 1 ||
         rows->total < 1 || rows->max_rows < 1 || max_len < 0 || window < 0 || q_heads % cache->heads)
         return 0;
     return avae::attn_q8_workspace_bytes(rows->seqs, rows->total, rows->max_rows, max_len, q_heads,
-                                         cache->heads, cache->dim, window);
+                                         cache->heads, cache->dim, elem_size(dtype), window);
 }
 
 extern "C" int avae_attn_q8(const void* q, long long q_tok, long long q_head, int q_heads,
@@ -303,7 +303,7 @@ extern "C" int avae_attn_q8(const void* q, long long q_tok, long long q_head, in
         return abi_fail(AVAE_EINVAL, "%s: first is not aligned to 4 bytes", who);
     AVAE_CHECK(check_strides(who, "q", q_tok, q_head, r.total, q_heads, c.dim));
     const size_t need = avae::attn_q8_workspace_bytes(r.seqs, r.total, r.max_rows, max_len, q_heads,
-                                                      c.heads, c.dim, window);
+                                                      c.heads, c.dim, elem_size(dtype), window);
     if (need && (!workspace || ws_bytes < need || misaligned(workspace, 16)))
         return abi_fail(AVAE_EWORKSPACE, "%s: %zu bytes of workspace, aligned to 16, are needed",
                         who, need);

@@ -187,7 +187,7 @@ struct AttnQ8 {
     float scale;
 };
 size_t attn_q8_workspace_bytes(int seqs, int total, int max_rows, int max_len, int q_heads,
-                               int heads, int dim, int window);
+                               int heads, int dim, int elem, int window);
 hipError_t launch_attn_q8(int dtype, const AttnQ8& a, const CacheQ8& c, const Ragged& r, void* ws,
                           hipStream_t stream);
 

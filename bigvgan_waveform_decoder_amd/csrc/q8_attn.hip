@@ -178,14 +178,21 @@ struct Query {
 
 constexpr int kWaves = 4;
 
+// Waves a SIMD of the kernel for few rows: as many as its registers allow
+// without spills, for the bytes in flight.
+constexpr int few_residency(int dim, int elem) {
+    return dim > 128 ? 2 : elem == 4 && dim == 128 ? 3 : 4;
+}
+
 // Few query rows: one tile of 16 rows a workgroup, the keys of one chunk
 // dealt to its waves 32 at a time, straight from memory to the matrix cores'
 // registers.  Each wave keeps its own maximum, sum and output; they are
 // joined in LDS, and where the keys are split over workgroups a second
 // kernel joins the chunks.  HBM-bound: the cache is read once.
 template <typename T, int D>
-__global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, CacheQ8 c, Ragged r,
-                                                                  int splits, int chunk,
+__global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn_q8_few_kernel(AttnQ8 a, CacheQ8 c, Ragged r,
+                                                                  int splits, int chunk, int span,
+                                                                  int pieces, int pairs,
                                                                   float* part) {
     constexpr bool kSplit = Query<T, D>::kSplit;
     constexpr int DT = D / 16;  // output tiles
@@ -193,8 +200,11 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, Cach
     __shared__ float s_out[kWaves * 16 * LD];
     __shared__ float s_m[kWaves * 16], s_l[kWaves * 16];
     const int lane = threadIdx.x & 63, wave = wave_id(), n16 = lane & 15, g = lane >> 4;
-    const int b = blockIdx.z, head = blockIdx.y;
-    const int split = blockIdx.x % splits, tile = blockIdx.x / splits;
+    // Sequences, heads and tiles side by side, chunks after one another:
+    // workgroups go to the XCDs in turn, and the last chunks may be empty.
+    const int all = r.seqs * pairs;
+    const int split = blockIdx.x / all, in_all = blockIdx.x % all;
+    const int b = in_all / pairs, tile = in_all % pairs / c.heads, head = in_all % c.heads;
     int cu0, n, len;
     if (!ragged_rows(r, b, cu0, n, len)) {
         if (cu0 < 0 || n <= 0 || cu0 + (long long)n > r.total) return;
@@ -202,18 +212,32 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, Cach
     }
     const int group = a.q_heads / c.heads;
     if (tile * 16 >= n * group) return;
+    if (pieces) {
+        // The host cut by the longest sequence; what there is in all gives
+        // shorter chunks, as many as it left room for.
+        long long keys = 0;
+        for (int i = lane; i < r.seqs; i += 64) keys += min(max(r.lens[i], 0), span);
+        for (int o = 32; o > 0; o >>= 1) keys += __shfl_xor(keys, o);
+        const long long even = (keys * pairs + pieces - 1) / pieces;
+        const int least = (span + splits - 1) / splits;
+        chunk = (min(chunk, max((int)min(even, (long long)chunk), least)) + 127) & ~127;
+    }
     const Row row = row_of(a, c, b, head, cu0, n, len, tile * 16 + n16);
     int any_lo, any_hi, all_lo, all_hi;
     tile_bounds(row, any_lo, any_hi, all_lo, all_hi);
     const int base = any_lo < any_hi ? (any_lo & ~31) : 0;
     const int t_lo = base + split * chunk, t_hi = min(t_lo + chunk, any_hi);
 
-    Query<T, D> q;
-    q.load(a, row, g);
-    const float to_log2 = q.back * a.scale * kLog2e;
+    if (splits > 1 && t_lo >= t_hi) {  // a chunk without keys
+        if (threadIdx.x < 16 && row.live) {
+            float* pr = part + (((long long)row.tok * a.q_heads + row.q_head) * splits + split) *
+                                   (D + 4);
+            pr[0] = neg_inf();
+            pr[1] = 0.0f;
+        }
+        return;
+    }
 
-    f4 acc[DT] = {};
-    float m = neg_inf(), l = 0.0f, v_run = 0.0f;
     // the table entries of a step, read a step ahead of their use
     int entry[2];
     auto look_up = [&](int t0) {
@@ -221,6 +245,12 @@ __global__ __launch_bounds__(64 * kWaves) void attn_q8_few_kernel(AttnQ8 a, Cach
         entry[1] = page_entry(c, b, (t0 + 16) >> c.shift);
     };
     look_up(t_lo + 32 * wave);
+    Query<T, D> q;
+    q.load(a, row, g);
+    const float to_log2 = q.back * a.scale * kLog2e;
+
+    f4 acc[DT] = {};
+    float m = neg_inf(), l = 0.0f, v_run = 0.0f;
     for (int t0 = t_lo + 32 * wave; t0 < t_hi; t0 += 32 * kWaves) {
         f4 s[2];
         float vs[2];
@@ -733,96 +763,128 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
     }
 }
 
-// Joins the chunks of one output row: a thread for four dims, the chunks
-// dealt to the workgroup's lanes beyond them.
+constexpr int kMaxSplits = 4224;  // over what the cut below can ask for
+
+// Joins the chunks of one output row: first their weights, then the weighted
+// sum, a thread for four dims and the chunks dealt to the workgroup's lanes.
 template <typename T, int D>
-__global__ __launch_bounds__(256) void attn_q8_join_kernel(AttnQ8 a, int splits,
+__global__ __launch_bounds__(512) void attn_q8_join_kernel(AttnQ8 a, int splits,
                                                            const float* __restrict__ part) {
-    constexpr int COLS = D / 4, LANES = 256 / COLS;
-    __shared__ f4 s_out[256];
-    __shared__ float s_m[256], s_l[256];
+    constexpr int COLS = D / 4, LANES = 512 / COLS;
+    __shared__ float s_by[kMaxSplits];
+    __shared__ f4 s_out[512];
+    __shared__ float s_m[8], s_l[8];
     const long long row = blockIdx.x;
-    const int col = threadIdx.x % COLS, at = threadIdx.x / COLS;
     const float* pr = part + row * splits * (D + 4);
-    float m = neg_inf(), l = 0.0f;
+    float m = neg_inf();
+    for (int s = threadIdx.x; s < splits; s += 512) {
+        const float pm = pr[(long long)s * (D + 4)];
+        s_by[s] = pm;
+        m = fmaxf(m, pm);
+    }
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if ((threadIdx.x & 63) == 0) s_m[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, s_m[w]);
+    const float at = m == neg_inf() ? 0.0f : m;
+    float l = 0.0f;
+    for (int s = threadIdx.x; s < splits; s += 512) {
+        const float pm = s_by[s], pl = pr[(long long)s * (D + 4) + 1];
+        // a chunk without keys has written nothing else
+        const float by = pm == neg_inf() && pl == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(pm - at);
+        s_by[s] = by;
+        l += by == 0.0f ? 0.0f : by * pl;
+    }
+    l = wave_sum(l);
+    if ((threadIdx.x & 63) == 0) s_l[threadIdx.x >> 6] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) l += s_l[w];
+    const int col = threadIdx.x % COLS;
     f4 o = {};
-    for (int s = at; s < splits; s += LANES) {
-        const float pm = pr[s * (D + 4)], pl = pr[s * (D + 4) + 1];
-        const f4 po = *reinterpret_cast<const f4*>(pr + s * (D + 4) + 4 + 4 * col);
-        if (pm == neg_inf() && pl == 0.0f) continue;  // the chunk has no key of this row
-        const float m_new = fmaxf(m, pm);
-        const float old = __builtin_amdgcn_exp2f(m - m_new), now = __builtin_amdgcn_exp2f(pm - m_new);
-        l = l * old + pl * now;
-        o = o * old + po * now;
-        m = m_new;
+#pragma unroll 4
+    for (int s = threadIdx.x / COLS; s < splits; s += LANES) {
+        const float by = s_by[s];
+        f4 x = *reinterpret_cast<const f4*>(pr + (long long)s * (D + 4) + 4 + 4 * col);
+        if (by == 0.0f) x = (f4){};
+        o += by * x;
     }
     s_out[threadIdx.x] = o;
-    s_m[threadIdx.x] = m;
-    s_l[threadIdx.x] = l;
     __syncthreads();
-    if (at != 0) return;
-    float top = m;
-    for (int k = 1; k < LANES; ++k) top = fmaxf(top, s_m[k * COLS + col]);
-    const float ref = top == neg_inf() ? 0.0f : top;
-    float sum = 0.0f;
-    f4 out = {};
-    for (int k = 0; k < LANES; ++k) {
-        const float by = __builtin_amdgcn_exp2f(s_m[k * COLS + col] - ref);
-        sum += by * s_l[k * COLS + col];
-        out += by * s_out[k * COLS + col];
-    }
-    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (threadIdx.x >= COLS) return;
+#pragma unroll
+    for (int k = 1; k < LANES; ++k) o += s_out[k * COLS + col];
+    const float by = l == 0.0f ? 0.0f : 1.0f / l;
     Pack<T, 4> y;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y.v[j] = round_to<T>(out[j] * by);
+    for (int j = 0; j < 4; ++j) y.v[j] = round_to<T>(o[j] * by);
     *reinterpret_cast<Pack<T, 4>*>((T*)a.out + row * D + 4 * col) = y;
-    if (a.lse && col == 0) a.lse[row] = lse_of(top, sum);
+    if (a.lse && col == 0) a.lse[row] = lse_of(m, l);
 }
 
-// How the rows are tiled and the keys of a tile cut: about kChunks pieces in
-// all, of at least a step each.  The lengths are on the device, so this goes
-// by the longest; pieces past a sequence's end are empty.
+// How the rows are tiled and the keys of a tile cut.  The lengths are on the
+// device, so this goes by the longest; chunks past a sequence's end are
+// empty.
 struct Cut {
     bool many;  // the kernel for many rows
     int tiles, splits, chunk;
+    int span;    // keys of one row tile at most, from an aligned start
+    int pieces;  // few rows: chunks in all to aim at, 0 for the chunk as it is
 };
 
-Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int window) {
+int round_up_to(long long x, int step) { return (int)((x + step - 1) / step * step); }
+
+Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int dim, int elem,
+        int window) {
     const int group = q_heads / heads;
     const long long rows = (long long)max_rows * group;
     Cut r;
     r.many = rows > 32;
-    const int height = r.many ? 32 * kWaves : 16;
-    const int step = r.many ? 64 : 32 * kWaves;
-    const int pieces = r.many ? 768 : 4096;
+    const int height = r.many ? 32 * kWaves : 16, step = r.many ? 64 : 32 * kWaves;
     r.tiles = (int)((rows + height - 1) / height);
-    long long span = max_len;  // keys of one row tile, from an aligned start
-    if (window > 0) span = std::min<long long>(span, (long long)window + height / group + 65);
-    const long long all = span * seqs * heads * r.tiles;
-    long long chunk = (all / pieces + step - 1) / step * step;
-    if (r.many) chunk = std::max<long long>(chunk, 512);
-    chunk = std::min(std::max<long long>(chunk, step), (span + step - 1) / step * step);
-    r.chunk = (int)std::max<long long>(chunk, step);
-    r.splits = (int)std::max<long long>(1, (span + r.chunk - 1) / r.chunk);
+    r.span = max_len;
+    if (window > 0)
+        r.span = (int)std::min<long long>(r.span, (long long)window + height / group + 65);
+    const long long pairs = (long long)seqs * heads * r.tiles;
+    r.pieces = 0;
+    if (r.many) {
+        r.chunk = std::max(round_up_to(r.span * pairs / 768, step), 512);
+    } else {
+        // One resident round of workgroups: every one pays for its start
+        // ([64 x 12000 keys, 4 heads of 128]: 1024 chunks 151 us, 2048 156,
+        // 4096 169).
+        const int resident = 256 * few_residency(dim, elem);
+        r.chunk = std::max(round_up_to((r.span * pairs + resident - 1) / resident, step), step);
+        if (seqs > 1 && seqs <= 1024) r.pieces = resident;
+    }
+    r.chunk = std::min(r.chunk, std::max(round_up_to(r.span, step), step));
+    r.splits = std::max((r.span + r.chunk - 1) / r.chunk, 1);
+    if (r.pieces)  // room for chunks half as long where lengths differ
+        r.splits = std::max(std::min(2 * r.splits, (r.span + step - 1) / step), 1);
     return r;
 }
 
 template <typename T, int D>
 hipError_t run(const AttnQ8& a, const CacheQ8& c, const Ragged& r, float* part,
                hipStream_t stream) {
-    const Cut k = cut(r.seqs, r.max_rows, a.max_len, a.q_heads, c.heads, a.window);
+    const Cut k = cut(r.seqs, r.max_rows, a.max_len, a.q_heads, c.heads, D, sizeof(T), a.window);
+    const long long blocks = (long long)k.tiles * k.splits * c.heads * r.seqs;
+    if (blocks > 0xffffff) return hipErrorInvalidValue;  // 2^32 threads
     if (k.many)
         hipLaunchKernelGGL((attn_q8_many_kernel<T, D>),
-                           dim3((unsigned)(k.tiles * k.splits * c.heads * r.seqs)),
+                           dim3((unsigned)blocks),
                            dim3(64 * kWaves), 0, stream, a, c, r, k.splits, k.chunk, k.tiles, part);
     else
         hipLaunchKernelGGL((attn_q8_few_kernel<T, D>),
-                           dim3((unsigned)(k.tiles * k.splits), c.heads, r.seqs),
-                           dim3(64 * kWaves), 0, stream, a, c, r, k.splits, k.chunk, part);
+                           dim3((unsigned)blocks),
+                           dim3(64 * kWaves), 0, stream, a, c, r, k.splits, k.chunk, k.span,
+                           k.pieces, c.heads * k.tiles, part);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && k.splits > 1) {
         hipLaunchKernelGGL((attn_q8_join_kernel<T, D>), dim3((unsigned)(r.total * a.q_heads)),
-                           dim3(256), 0, stream, a, k.splits, part);
+                           dim3(512), 0, stream, a, k.splits, part);
         e = hipGetLastError();
     }
     return e;
@@ -839,8 +901,8 @@ hipError_t attn_q8(const AttnQ8& a, const CacheQ8& c, const Ragged& r, float* pa
 }  // namespace
 
 size_t attn_q8_workspace_bytes(int seqs, int total, int max_rows, int max_len, int q_heads,
-                               int heads, int dim, int window) {
-    const Cut k = cut(seqs, max_rows, max_len, q_heads, heads, window);
+                               int heads, int dim, int elem, int window) {
+    const Cut k = cut(seqs, max_rows, max_len, q_heads, heads, dim, elem, window);
     return k.splits > 1 ? (size_t)total * q_heads * k.splits * (dim + 4) * sizeof(float) : 0;
 }
 

@@ -641,7 +641,7 @@ int avae_kv_read_q8(const avae_kv_q8* cache, const avae_ragged* rows, int dtype,
  *   EWORKSPACE.
  */
 size_t avae_attn_q8_workspace_bytes(const avae_kv_q8* cache, const avae_ragged* rows, int q_heads,
-                                    int max_len, int window);
+                                    int dtype, int max_len, int window);
 int avae_attn_q8(const void* q, long long q_tok, long long q_head, int q_heads, int dtype,
                  const avae_kv_q8* cache, const avae_ragged* rows, const int* first, int max_len,
                  float scale, int causal, int window, void* out, float* lse, void* workspace,

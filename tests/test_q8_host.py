@@ -153,9 +153,9 @@ def test_attention_workspace():
     c = _cache(n_pages=1000)
     r = _rows(table_cols=500, table_ld=500, seqs=1, total=1, max_rows=1)
     pc, pr = ctypes.byref(c), ctypes.byref(r)
-    assert L.avae_attn_q8_workspace_bytes(None, pr, 4, 100, 0) == 0
-    assert L.avae_attn_q8_workspace_bytes(pc, pr, 3, 100, 0) == 0
-    need = L.avae_attn_q8_workspace_bytes(pc, pr, 4, 8000, 0)
+    assert L.avae_attn_q8_workspace_bytes(None, pr, 4, 1, 100, 0) == 0
+    assert L.avae_attn_q8_workspace_bytes(pc, pr, 3, 1, 100, 0) == 0
+    need = L.avae_attn_q8_workspace_bytes(pc, pr, 4, 1, 8000, 0)
     if need:
         for kw in (dict(ws_bytes=need - 1), dict(ws=None), dict(ws=ODD)):
             assert _attn(cache=c, rows=r, max_len=8000, **kw) == EWORKSPACE
