@@ -824,6 +824,47 @@ __global__ __launch_bounds__(512) void attn_q8_join_kernel(AttnQ8 a, int splits,
     if (a.lse && col == 0) a.lse[row] = lse_of(m, l);
 }
 
+// The same for up to 64 chunks, a wave a row: a lane for a chunk's weight,
+// then for four dims of some of them.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attn_q8_join_few_kernel(AttnQ8 a, int rows, int splits,
+                                                               const float* __restrict__ part) {
+    constexpr int COLS = D / 4, LANES = 64 / COLS;
+    const int lane = threadIdx.x & 63;
+    const long long row = blockIdx.x * 4LL + wave_id();
+    if (row >= rows) return;
+    const float* pr = part + row * splits * (D + 4);
+    float m = neg_inf(), l = 0.0f;
+    if (lane < splits) {
+        m = pr[(long long)lane * (D + 4)];
+        l = pr[(long long)lane * (D + 4) + 1];
+    }
+    float top = m;
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    const float at = top == neg_inf() ? 0.0f : top;
+    // a chunk without keys has written nothing else
+    const float by = m == neg_inf() && l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - at);
+    l = wave_sum(by == 0.0f ? 0.0f : by * l);
+    const int col = lane % COLS;
+    f4 o = {};
+    for (int s0 = 0; s0 < splits; s0 += LANES) {
+        const int s = s0 + lane / COLS;
+        const float w = s < splits ? __shfl(by, s) : 0.0f;
+        if (w != 0.0f)
+            o += w * *reinterpret_cast<const f4*>(pr + (long long)s * (D + 4) + 4 + 4 * col);
+    }
+    for (int i = COLS; i < 64; i <<= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] += __shfl_xor(o[j], i);
+    if (lane >= COLS) return;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    Pack<T, 4> y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y.v[j] = round_to<T>(o[j] * inv);
+    *reinterpret_cast<Pack<T, 4>*>((T*)a.out + row * D + 4 * col) = y;
+    if (a.lse && col == 0) a.lse[row] = lse_of(top, l);
+}
+
 // How the rows are tiled and the keys of a tile cut.  The lengths are on the
 // device, so this goes by the longest; chunks past a sequence's end are
 // empty.
@@ -850,7 +891,10 @@ Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int dim, in
     const long long pairs = (long long)seqs * heads * r.tiles;
     r.pieces = 0;
     if (r.many) {
-        r.chunk = std::max(round_up_to(r.span * pairs / 768, step), 512);
+        // split where that leaves CUs busy that would have none, in chunks
+        // of 512 keys or more
+        const long long parts = std::max(std::min(768 / pairs, (long long)r.span / 512), 1LL);
+        r.chunk = std::max(round_up_to((r.span + parts - 1) / parts, step), step);
     } else {
         // One resident round of workgroups: every one pays for its start
         // ([64 x 12000 keys, 4 heads of 128]: 1024 chunks 151 us, 2048 156,
@@ -883,8 +927,13 @@ hipError_t run(const AttnQ8& a, const CacheQ8& c, const Ragged& r, float* part,
                            k.pieces, c.heads * k.tiles, part);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && k.splits > 1) {
-        hipLaunchKernelGGL((attn_q8_join_kernel<T, D>), dim3((unsigned)(r.total * a.q_heads)),
-                           dim3(512), 0, stream, a, k.splits, part);
+        const int rows = r.total * a.q_heads;
+        if (k.splits <= 64)
+            hipLaunchKernelGGL((attn_q8_join_few_kernel<T, D>), dim3((unsigned)(rows + 3LL) / 4),
+                               dim3(256), 0, stream, a, rows, k.splits, part);
+        else
+            hipLaunchKernelGGL((attn_q8_join_kernel<T, D>), dim3((unsigned)rows), dim3(512), 0,
+                               stream, a, k.splits, part);
         e = hipGetLastError();
     }
     return e;
