@@ -6,4 +6,4 @@ binding with the same entry-point names.  Importing the package itself loads
 nothing: the binding loads the library on first use and raises if it is
 missing.
 """
-__all__ = ["avae", "workloads"]
+__all__ = ["avae", "latents", "workloads"]
