@@ -891,9 +891,11 @@ Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int dim, in
     const long long pairs = (long long)seqs * heads * r.tiles;
     r.pieces = 0;
     if (r.many) {
-        // split where that leaves CUs busy that would have none, in chunks
-        // of 512 keys or more
-        const long long parts = std::max(std::min(768 / pairs, (long long)r.span / 512), 1LL);
+        // Split only to give every CU a workgroup, in chunks of 128 keys or
+        // more: the joined parts are float32 rows ([4 x 512 rows, 1000 keys,
+        // 12 heads], 192 workgroups: 43 us whole, 52 in two parts; [5 x 17
+        // rows, window 513, 2 heads], 20 workgroups: 26 whole, 21 in four).
+        const long long parts = std::max(std::min(256 / pairs, (long long)r.span / 128), 1LL);
         r.chunk = std::max(round_up_to((r.span + parts - 1) / parts, step), step);
     } else {
         // One resident round of workgroups: every one pays for its start

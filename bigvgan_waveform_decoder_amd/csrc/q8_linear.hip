@@ -32,16 +32,28 @@ struct LinearQ8 {
     int yvec;  // outputs can be stored 16 bytes at a time
 };
 
-// 16 bytes of a row from k on; zeros from K on.  AL: the address is a
-// multiple of 16.
+// 16 bytes of a row from k on.  AL: the address is a multiple of 16.
+// Otherwise the aligned words that hold them are read (every word holds one
+// of the bytes, so none lies outside the row's memory) and shifted into
+// place: a load from an odd address takes three times as long
+// ([37, 1535, 6143]: 36 us against 11 aligned).
 template <bool AL>
 __device__ inline v4i load16(const int8_t* row, int k) {
     if (AL) return *reinterpret_cast<const v4i*>(row + k);
-    v4i v;
-    __builtin_memcpy(&v, row + k, 16);
-    return v;
+    const uintptr_t at = (uintptr_t)(row + k);
+    const unsigned shift = (unsigned)at & 3;
+    struct alignas(4) Words {
+        unsigned w[4];
+    };
+    const Words x = *reinterpret_cast<const Words*>(at & ~(uintptr_t)3);
+    const unsigned last = *reinterpret_cast<const unsigned*>((at + 15) & ~(uintptr_t)3);
+    return (v4i){(int)__builtin_amdgcn_alignbyte(x.w[1], x.w[0], shift),
+                 (int)__builtin_amdgcn_alignbyte(x.w[2], x.w[1], shift),
+                 (int)__builtin_amdgcn_alignbyte(x.w[3], x.w[2], shift),
+                 (int)__builtin_amdgcn_alignbyte(last, x.w[3], shift)};
 }
 
+// The same with zeros from K on.
 __device__ inline v4i load16_tail(const int8_t* row, int k, int K) {
     v4i v;
     for (int i = 0; i < 4; ++i) {
@@ -86,6 +98,8 @@ __device__ inline void store4(const LinearQ8& p, int m, int n, v4i acc, const Sc
         out.v[r] = round_to<T>(epilogue<SILU>(acc[r], s.sa, s.sw[r], s.bias[r]));
     if (p.yvec) {
         *reinterpret_cast<Pack<T, 4>*>(y) = out;
+    } else if (n + 4 <= p.N) {
+        __builtin_memcpy(y, &out, sizeof(out));
     } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -255,7 +269,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void linear_q8_tile_kernel(LinearQ8 
                                                                   piece(j) * 1024),
                         16, 0, 0);
                 else
-                    reg[q * (JA + JW) + j] = load16<false>(from + off, 0);
+                    __builtin_memcpy(&reg[q * (JA + JW) + j], from + off, 16);
             }
     };
     auto stage_end = [&](int8_t* s) {
@@ -386,6 +400,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void linear_q8_tile_kernel(LinearQ8 
                                                           sw[c + e], bias[c + e]));
                 if (p.yvec) {
                     if (c < ends) *reinterpret_cast<Pack<T, E>*>(y + c) = out;
+                } else if (c + E <= ends) {
+                    __builtin_memcpy(y + c, &out, sizeof(out));
                 } else {
 #pragma unroll
                     for (int e = 0; e < E; ++e)
@@ -394,6 +410,19 @@ __global__ __launch_bounds__(WGM* WGN * 64) void linear_q8_tile_kernel(LinearQ8 
             }
         }
     }
+}
+
+// Rows of K bytes at any address to rows of `width` bytes, a multiple of 128,
+// with zeros behind them: what the tiles are staged from by DMA.  A wave a
+// row, the activations' first.
+__global__ __launch_bounds__(256) void pack_q8_kernel(LinearQ8 p, int8_t* __restrict__ out,
+                                                      int width) {
+    const long long row = blockIdx.x * 4LL + (threadIdx.x >> 6);
+    if (row >= (long long)p.M + p.N) return;
+    const int8_t* from = row < p.M ? p.a + row * p.lda : p.w + (row - p.M) * p.ldw;
+    for (int k = (threadIdx.x & 63) * 16; k < width; k += 1024)
+        *reinterpret_cast<v4i*>(out + row * width + k) =
+            k + 16 <= p.K ? load16<false>(from, k) : load16_tail(from, k, p.K);
 }
 
 constexpr int kCus = 256;
@@ -419,39 +448,42 @@ hipError_t run_tile(const LinearQ8& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-long long tiles(const LinearQ8& p, int bm, int bn) {
-    return (long long)((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn);
+long long tiles(int M, int N, int bm, int bn) {
+    return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn);
 }
+
+// Whether the rows kernel takes a product.  It re-reads an operand for each
+// 64 x 32 outputs; from more of those than CUs on, the tiles win
+// ([128, 6144, 1536]: 12.5 against 8.5 us; [300, 1536, 6144], 240
+// workgroups: 20.1 against 22).
+bool by_rows(int M, int N) { return M <= 16 || tiles(M, N, 64, 32) <= kCus; }
 
 // Which kernel: by the workgroups that each makes of M x N (times measured on
 // [M, N, K], bfloat16 output).
 template <typename T, bool SILU, bool AL>
 hipError_t run(const LinearQ8& p, hipStream_t stream) {
-    // Offsets inside a tile are 32 bits.  The rows kernel re-reads an operand
-    // for each 64 x 32 outputs; from more of those than CUs on, the tiles
-    // win ([128, 6144, 1536]: 12.5 against 8.5 us; [300, 1536, 6144], 240
-    // workgroups: 20.1 against 22).
-    const bool fits = p.lda < (1 << 22) && p.ldw < (1 << 22);
-    if (p.M <= 16 || tiles(p, 64, 32) <= kCus || !fits) {
+    const auto tiles = [&](int bm, int bn) { return avae::tiles(p.M, p.N, bm, bn); };
+    // (offsets inside a tile are 32 bits)
+    if (by_rows(p.M, p.N) || p.lda >= (1 << 22) || p.ldw >= (1 << 22)) {
         // the largest tiles that leave at least 144 workgroups
         // ([37, 1536, 6144]: 16 x 16 12.1 us, 32 x 16 11.1, 32 x 32 13.8;
         // [37, 6144, 1536]: 16 x 16 10.9, 32 x 16 9.6, 64 x 32 6.7)
-        if (p.M > 32 && tiles(p, 64, 32) >= 144) return run_rows<T, SILU, AL, 4, 2>(p, stream);
-        if (p.M > 16 && tiles(p, 32, 32) >= 144) return run_rows<T, SILU, AL, 2, 2>(p, stream);
-        if (p.M > 16 && tiles(p, 32, 16) >= 144) return run_rows<T, SILU, AL, 2, 1>(p, stream);
-        if (p.M <= 16 && tiles(p, 16, 32) >= 144) return run_rows<T, SILU, AL, 1, 2>(p, stream);
+        if (p.M > 32 && tiles(64, 32) >= 144) return run_rows<T, SILU, AL, 4, 2>(p, stream);
+        if (p.M > 16 && tiles(32, 32) >= 144) return run_rows<T, SILU, AL, 2, 2>(p, stream);
+        if (p.M > 16 && tiles(32, 16) >= 144) return run_rows<T, SILU, AL, 2, 1>(p, stream);
+        if (p.M <= 16 && tiles(16, 32) >= 144) return run_rows<T, SILU, AL, 1, 2>(p, stream);
         return run_rows<T, SILU, AL, 1, 1>(p, stream);
     }
     if constexpr (AL) {
         // up to two 64 x 64 tiles a CU ([1000, 1536, 1536]: 11.0 us, 64 x 128
         // 12.7; [512, 6144, 1536], three a CU: 18.9 against 15.1)
-        if (tiles(p, 64, 64) <= 2 * kCus) return run_tile<T, SILU, true, 2, 1, 2, 2>(p, stream);
+        if (tiles(64, 64) <= 2 * kCus) return run_tile<T, SILU, true, 2, 1, 2, 2>(p, stream);
         // the large tiles fill the CUs in rounds; a 64 x 128 one costs half
         // as much again for its area, but leaves no CU idle
         // ([6000, 6144, 1536]: 256 x 256 103 us, 192 x 256 87, 64 x 128 104;
         // [8192, 8192, 8192]: 476, 532, 713; [2048, 1536, 6144]: 78, 64, 38)
         const auto rounds = [&](int bm) {
-            return (double)((tiles(p, bm, 256) + kCus - 1) / kCus) * bm * 256;
+            return (double)((tiles(bm, 256) + kCus - 1) / kCus) * bm * 256;
         };
         const double small = 1.5 * p.M * p.N / kCus;
         if (rounds(256) < rounds(192) && rounds(256) < small)
@@ -462,14 +494,32 @@ hipError_t run(const LinearQ8& p, hipStream_t stream) {
 }
 
 template <typename T, bool SILU>
-hipError_t linear_q8(const LinearQ8& p, hipStream_t stream) {
+hipError_t linear_q8(LinearQ8 p, void* ws, hipStream_t stream) {
     const bool al = (((uintptr_t)p.a | (uintptr_t)p.w | p.lda | p.ldw) & 15) == 0;
-    return al ? run<T, SILU, true>(p, stream) : run<T, SILU, false>(p, stream);
+    if (al) return run<T, SILU, true>(p, stream);
+    if (linear_q8_workspace_bytes(p.M, p.N, p.K) == 0) return run<T, SILU, false>(p, stream);
+    // large and not aligned: laid out anew for the DMA, which pays from the
+    // first tiles on ([6000, 6143, 1535]: 104 us, 285 straight from memory)
+    int8_t* rows = (int8_t*)ws;
+    const int width = (p.K + 127) / 128 * 128;
+    hipLaunchKernelGGL(pack_q8_kernel, dim3((unsigned)(((long long)p.M + p.N + 3) / 4)), dim3(256),
+                       0, stream, p, rows, width);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    p.a = rows;
+    p.w = rows + (long long)p.M * width;
+    p.lda = p.ldw = p.K = width;
+    return run<T, SILU, true>(p, stream);
 }
 
 }  // namespace
 
-size_t linear_q8_workspace_bytes(int M, int N, int K) { return 0; }
+// Rows whose length is no multiple of 16 bytes are laid out anew where the
+// product is large enough for tiles.
+size_t linear_q8_workspace_bytes(int M, int N, int K) {
+    if (K % 16 == 0 || by_rows(M, N)) return 0;
+    return ((size_t)M + N) * ((K + 127) / 128 * 128);
+}
 
 hipError_t launch_linear_q8(const int8_t* a, long long lda, const float* sa, const int8_t* w,
                             long long ldw, const float* sw, const float* bias, int M, int N, int K,
@@ -481,11 +531,11 @@ hipError_t launch_linear_q8(const int8_t* a, long long lda, const float* sa, con
     prof_pre(stream);
     hipError_t e;
     if (dtype == AVAE_F32)
-        e = act ? linear_q8<float, true>(p, stream) : linear_q8<float, false>(p, stream);
+        e = act ? linear_q8<float, true>(p, ws, stream) : linear_q8<float, false>(p, ws, stream);
     else if (dtype == AVAE_BF16)
-        e = act ? linear_q8<__bf16, true>(p, stream) : linear_q8<__bf16, false>(p, stream);
+        e = act ? linear_q8<__bf16, true>(p, ws, stream) : linear_q8<__bf16, false>(p, ws, stream);
     else
-        e = act ? linear_q8<_Float16, true>(p, stream) : linear_q8<_Float16, false>(p, stream);
+        e = act ? linear_q8<_Float16, true>(p, ws, stream) : linear_q8<_Float16, false>(p, ws, stream);
     prof_post(stream, "linear_q8_kernel", 2.0 * M * N * K,
               (double)M * K + (double)N * K + (double)M * N * es);
     return e;
