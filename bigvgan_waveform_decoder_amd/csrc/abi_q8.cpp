@@ -81,8 +81,8 @@ int check_ragged(const char* who, const avae_ragged* r, CacheQ8* c, Ragged* out)
     if (r->seqs > 0 && (r->table_cols < 1 || r->table_ld < r->table_cols))
         return abi_fail(AVAE_ESHAPE, "%s: table of %d columns at a row stride of %lld", who,
                         r->table_cols, r->table_ld);
-    if ((long long)r->table_cols * c->page > (1 << 30))
-        return abi_fail(AVAE_ESHAPE, "%s: a table row covers more than 2^30 tokens", who);
+    if ((long long)r->table_cols * c->page > (1 << 29))
+        return abi_fail(AVAE_ESHAPE, "%s: a table row covers more than 2^29 tokens", who);
     if (r->table_ld > kMaxElems / 65536)
         return abi_fail(AVAE_ESHAPE, "%s: the table is too large", who);
     if (r->max_rows > r->total)
@@ -317,7 +317,7 @@ extern "C" int avae_attn_q8(const void* q, long long q_tok, long long q_head, in
     a.q_heads = q_heads;
     a.max_len = max_len;
     a.causal = causal ? 1 : 0;
-    a.window = window;
+    a.window = window < (1 << 30) ? window : 1 << 30;
     a.scale = scale;
     return done(avae::launch_attn_q8(dtype, a, c, r, workspace, (hipStream_t)stream), who);
 }

@@ -120,7 +120,8 @@ __device__ inline Row row_of(const AttnQ8& a, const CacheQ8& c, int b, int head,
     r.q_head = head * group + (r.live ? row - i * group : 0);
     const int pos = len - n + i;
     const int first = a.first ? max(a.first[b], 0) : 0;
-    r.hi = r.live ? max(a.causal ? pos + 1 : len, 0) : 0;
+    // (a length past the table adds no key)
+    r.hi = r.live ? min(max(a.causal ? pos + 1 : len, 0), c.table_cols << c.shift) : 0;
     r.lo = min(a.window ? max(first, pos - a.window + 1) : first, r.hi);
     return r;
 }

@@ -576,6 +576,7 @@ typedef struct avae_kv_q8 {
 
 /*
  * Packed rows of `seqs` sequences (all pointers DEVICE memory, int32).
+ *   (at most 2^29 tokens a table row, 2^30 packed rows, 65535 sequences)
  *   cu [seqs + 1]: rows cu[b] .. cu[b+1] of the packed tensors are the LAST
  *     cu[b+1] - cu[b] tokens of sequence b, in order; none if they are equal.
  *   lens [seqs]: tokens of sequence b, these rows among them.

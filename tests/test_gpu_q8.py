@@ -609,3 +609,87 @@ def test_attention_many_rows(new, lens, heads, kv_heads, dim, page, window, dtyp
     _check_attention(c, new, heads, dtype, 11, window=window, first=first)
     if not window:
         _check_attention(c, new, heads, dtype, 12, causal=False, first=first)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_lengths_past_the_table(dtype):
+    """A length beyond the table's tokens adds no key: few and many rows."""
+    announce(f"attn_q8 lengths past the table {dtype}")
+    for new in ([1, 2], [60, 3]):
+        c = Cache(33, [64, 64], 2, 64, 16)
+        c.poison_unused()
+        c.table = np.ascontiguousarray(c.table[:, :4])
+        c.lens = np.array([1000, 70], np.int32)
+        _check_attention(c, new, 4, dtype, 2, max_len=64)
+
+
+def test_cache_beyond_32_bit_offsets():
+    """Pages whose first byte lies past 4 GiB of the cache."""
+    announce("kv_write_q8, kv_read_q8, attn_q8 past 4 GiB")
+    torch = _t()
+    from bigvgan_waveform_decoder_amd import avae
+    pages, page, dim = 270000, 128, 128  # 16 KiB a page
+    k8, v8 = (torch.empty((pages, 1, page, dim), dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty((pages, 1), device="cuda") for _ in range(2))
+    cache = avae.KvCacheQ8(k8, v8, ks, vs)
+    table = np.array([[269999, 262200, 5]], np.int32)
+    lens, cu = np.array([300], np.int32), np.array([0, 300], np.int32)
+    rng = np.random.default_rng(11)
+    k, v = (rng.normal(size=(300, 1, dim)).astype(np.float32) for _ in range(2))
+    args = (_dev(table), _dev(cu), _dev(lens))
+    avae.kv_write_q8(cache, _dev(k), _dev(v), *args)
+    small = {p: i for i, p in enumerate(table[0])}
+    t = np.array([[small[p] for p in table[0]]], np.int32)
+    q = [np.zeros((3, 1, page, dim), np.int8) for _ in range(2)]
+    s = [np.zeros((3, 1), np.float32) for _ in range(2)]
+    for i, x in enumerate((k, v)):
+        R.kv_write(q[i], s[i], x, t, cu, [300], 3, page)
+    rk, rv = avae.kv_read_q8(cache, *args, total=300)
+    assert np.array_equal(_np(rk), R.kv_read(q[0], s[0], t, cu, [300], page))
+    assert np.array_equal(_np(rv), R.kv_read(q[1], s[1], t, cu, [300], page))
+    for rows in (1, 300):
+        one = np.array([0, rows], np.int32)
+        x = rng.normal(size=(rows, 2, dim)).astype(np.float32)
+        out = avae.attn_q8(_dev(x), cache, args[0], _dev(one), args[2])
+        ref = R.attention(x, q[0], s[0], q[1], s[1], t, one, [300], page, dim ** -0.5)[0]
+        assert np.abs(_np(out) - ref).max() <= 1e-4
+
+
+def test_calls_in_a_captured_graph():
+    """The calls allocate and synchronise nothing of their own: captured, and
+    replayed with other work between the replays, they give the eager bits."""
+    torch = _t()
+    from bigvgan_waveform_decoder_amd import avae
+    announce("8-bit operators in a graph")
+    lens, new = [700, 90], [1, 33]
+    c = Cache(34, lens, 2, 64, 16)
+    dev = c.upload()
+    cu = _cu(new)
+    args = (_dev(c.table), _dev(cu), _dev(c.lens))
+    rng = np.random.default_rng(5)
+    x, w = _dev(rng.normal(size=(34, 256)).astype(np.float32)), _dev(np.ones(256, np.float32))
+    pw, ps = avae.quant_q8(_dev(rng.normal(size=(8 * 64, 256)).astype(np.float32)))
+
+    def run():
+        q8, s, _ = avae.rms_norm_q8(x, w)
+        y = avae.linear_q8(q8, s, pw, ps, act="silu", dtype=torch.bfloat16)
+        q, k, v = y[:, :256], y[:, 256:384], y[:, 384:]
+        avae.kv_write_q8(dev, k.unflatten(1, (2, 64)), v.unflatten(1, (2, 64)), *args, max_new=33)
+        return avae.attn_q8(q.unflatten(1, (4, 64)), dev, *args, max_q=33, max_len=700)
+
+    want = run().clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run()
+    for _ in range(3):
+        got.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        assert torch.equal(run(), want)
