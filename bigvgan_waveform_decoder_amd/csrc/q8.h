@@ -98,6 +98,24 @@ __device__ inline void store_values(T* p, int left, const float (&x)[N]) {
     }
 }
 
+// 16 bytes of outputs that the caller reads back from memory: not kept in
+// the caches where the address allows the one store.
+template <typename T>
+__device__ inline void stream_values(T* p, int left, const float (&x)[16 / sizeof(T)]) {
+    constexpr int N = 16 / sizeof(T);
+    typedef unsigned u4 __attribute__((ext_vector_type(4), aligned(4)));
+    if (left >= N && ((uintptr_t)p & 3) == 0) {
+        T v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = round_to<T>(x[i]);
+        u4 w;
+        __builtin_memcpy(&w, v, 16);
+        __builtin_nontemporal_store(w, reinterpret_cast<u4*>(p));
+    } else {
+        store_values<N>(p, left, x);
+    }
+}
+
 template <int N>
 __device__ inline void store_bytes(int8_t* p, int left, const unsigned (&w)[N / 4]) {
     if (left >= N) {

@@ -105,7 +105,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_q8_kernel(
     }
 }
 
-// A wave a token: eight values a lane, of keys and of values.
+// A wave a token: 16 bytes of keys and of values a lane and step.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void kv_read_q8_kernel(CacheQ8 c, Ragged r,
                                                               T* __restrict__ k,
@@ -119,22 +119,23 @@ __global__ __launch_bounds__(kThreads) void kv_read_q8_kernel(CacheQ8 c, Ragged 
     const int page = pos >= 0 ? page_of(c, b, col) : -1;
     const int row = c.heads * c.dim, dim_shift = __builtin_ctz(c.dim);
     const long long out = (long long)(cu0 + i) * row;
-    for (int j = lane * 8; j < row; j += 512) {
-        float kv[8] = {}, vv[8] = {};
+    constexpr int N = 16 / sizeof(T);
+    for (int j = lane * N; j < row; j += 64 * N) {
+        float kv[N] = {}, vv[N] = {};
         if (page >= 0) {
             const long long at = (long long)page * c.heads + (j >> dim_shift);
             const long long e = (at * c.page + (pos & (c.page - 1))) * c.dim + (j & (c.dim - 1));
-            load_stored<8>(c.k + e, 8, kv);
-            load_stored<8>(c.v + e, 8, vv);
+            load_stored<N>(c.k + e, N, kv);
+            load_stored<N>(c.v + e, N, vv);
             const float ks = c.k_scale[at], vs = c.v_scale[at];
 #pragma unroll
-            for (int e8 = 0; e8 < 8; ++e8) {
-                kv[e8] *= ks;
-                vv[e8] *= vs;
+            for (int i = 0; i < N; ++i) {
+                kv[i] *= ks;
+                vv[i] *= vs;
             }
         }
-        store_values<8>(k + out + j, 8, kv);
-        store_values<8>(v + out + j, 8, vv);
+        stream_values(k + out + j, N, kv);
+        stream_values(v + out + j, N, vv);
     }
 }
 

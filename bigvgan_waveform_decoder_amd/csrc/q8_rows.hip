@@ -34,22 +34,38 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rows_q8_kernel(
     const long long row = THREADS == 64 ? blockIdx.x * 4LL + wave : blockIdx.x;
     if (row >= M) return;  // whole waves, and only where a wave has a row to itself
     const int tid = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
-    float v[HELD][8];
+    float v[HELD][8], r[RES ? HELD : 1][8];
     unsigned top = 0;
     float sq = 0.0f;
+    // all of the row is on its way before any of it is used
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+        const int c = (tid + j * THREADS) * 8;
+        load_values<8>(x + row * ldx + c, C - c, v[j]);
+    }
+    if (RES) {
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) {
+            const int c = (tid + j * THREADS) * 8;
+            load_values<8>(res + row * ldr + c, C - c, r[j]);
+        }
+    }
 #pragma unroll
     for (int j = 0; j < HELD; ++j) {
         const int c = (tid + j * THREADS) * 8, left = C - c;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-        if (left <= 0) continue;
-        load_values<8>(x + row * ldx + c, left, v[j]);
         if (RES) {
-            float r[8];
-            load_values<8>(res + row * ldr + c, left, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] += r[i];
-            store_values<8>(sum + row * lds + c, left, v[j]);
+            for (int i = 0; i < 8; ++i) v[j][i] += r[j][i];
+            // (next read a few operators later: streamed, [8192, 8192]
+            // bfloat16 105 -> 90 us)
+            constexpr int N = 16 / sizeof(T);
+#pragma unroll
+            for (int n = 0; n < 8; n += N) {
+                float part[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) part[i] = v[j][n + i];
+                stream_values(sum + row * lds + c + n, left - n, part);
+            }
         }
         if (NORM) {
             float g[8];
@@ -141,7 +157,7 @@ __global__ __launch_bounds__(1024) void long_rows_q8_kernel(
     }
 }
 
-// Eight values a thread; THREADS of them walk a row.
+// 16 bytes of output a thread; THREADS of them walk a row.
 template <typename T, int THREADS>
 __global__ __launch_bounds__(256) void dequant_q8_kernel(const int8_t* __restrict__ q,
                                                          long long ldq,
@@ -152,12 +168,13 @@ __global__ __launch_bounds__(256) void dequant_q8_kernel(const int8_t* __restric
     if (row >= M) return;
     const int tid = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
     const float s = scale[row];
-    for (int c = tid * 8; c < C; c += THREADS * 8) {
-        float v[8];
-        load_stored<8>(q + row * ldq + c, C - c, v);
+    constexpr int N = 16 / sizeof(T);
+    for (int c = tid * N; c < C; c += THREADS * N) {
+        float v[N];
+        load_stored<N>(q + row * ldq + c, C - c, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= s;
-        store_values<8>(y + row * ldy + c, C - c, v);
+        for (int i = 0; i < N; ++i) v[i] *= s;
+        stream_values(y + row * ldy + c, C - c, v);
     }
 }
 
@@ -173,15 +190,11 @@ hipError_t rows_q8(const void* x, long long ldx, const void* res, long long ldr,
                        dim3((unsigned)(THREADS == 64 ? (M + 3LL) / 4 : M)),                      \
                        dim3(THREADS < 256 ? 256 : THREADS), 0, stream, px, ldx, pr, ldr, w, M, C, \
                        eps, ps, lds, q, ldq, scale)
-    // A wave for a row where there are rows for all the CUs' waves, else a
-    // workgroup, which has less of the row to wait for.
-    const bool many = M >= 2048;
+    // A wave for a short row, which needs no barrier; a workgroup for others,
+    // where fewer bytes a lane leave more waves on the CUs ([6000, 1536]
+    // bfloat16 with residual: 17.2 us a wave a row, 14.3 so).
     if (C <= 512)
         AVAE_ROWS(64, 1);
-    else if (many && C <= 1024)
-        AVAE_ROWS(64, 2);
-    else if (many && C <= 2048)
-        AVAE_ROWS(64, 4);
     else if (C <= 2048)
         AVAE_ROWS(256, 1);
     else if (C <= 4096)
