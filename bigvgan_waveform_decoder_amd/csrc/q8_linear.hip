@@ -10,6 +10,14 @@
 // lane ends with consecutive n of one row m; with the weight rows dealt to
 // the tiles in fours (row 4 T (i / 4) + 4 t + i % 4 of T tiles to tile t) it
 // holds 4 T of them and stores them at once.
+//
+// Measured (bfloat16 output; the library's int8 product reaches 2330 TOPS at
+// [8192]^3): [8192, 8192, 8192] 484 us, 2270 TOPS, bound by LDS reads and
+// matrix instructions alike (1536 of LDS and 512 of staging cycles beside
+// 2048 of products a step); [6000, 6144, 1536] 80-83 us, whose twelve steps a
+// tile leave the outputs' writes and the SiLU of 96 values a thread a third
+// of the time; [37, 1536, 6144] 11.0 us and [1, 4608, 1536] 4.0 us (an empty
+// kernel takes 1.8): latency, with every load of a wave in flight at once.
 #include <algorithm>
 
 #include "avae.h"

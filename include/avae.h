@@ -563,7 +563,7 @@ int avae_linear_q8(const signed char* a, long long lda, const float* a_scale, co
  * A paged cache of keys and values in 8 bits, with one float32 scale for
  * each page and head.
  *   k, v: [n_pages, heads, page, dim] 8-bit, aligned to 16 bytes;
- *   k_scale, v_scale: [n_pages, heads] float32.
+ *   k_scale, v_scale: [n_pages, heads] float32, not negative.
  *   page: tokens a page, one of 16, 32, 64, 128, 256; dim: 64, 128 or 256.
  */
 typedef struct avae_kv_q8 {
