@@ -888,7 +888,7 @@ class _Env:
     def __init__(self):
         torch = _torch()
         L = lib()
-        self.empty = torch.empty
+        self.strided = torch.empty_strided  # the quickest of the allocators to call
         self.int8, self.int32, self.uint8 = torch.int8, torch.int32, torch.uint8
         self.float32 = torch.float32
         self.codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -898,6 +898,15 @@ class _Env:
         self.linear, self.linear_ws = L.avae_linear_q8, L.avae_linear_q8_workspace_bytes
         self.write, self.read = L.avae_kv_write_q8, L.avae_kv_read_q8
         self.attn, self.attn_ws = L.avae_attn_q8, L.avae_attn_q8_workspace_bytes
+
+    def vec(self, n, dtype, dev):
+        return self.strided((n,), (1,), dtype=dtype, device=dev)
+
+    def mat(self, m, n, dtype, dev):
+        return self.strided((m, n), (n, 1), dtype=dtype, device=dev)
+
+    def heads(self, t, h, d, dtype, dev):
+        return self.strided((t, h, d), (h * d, d, 1), dtype=dtype, device=dev)
 
     def code(self, dtype) -> int:
         code = self.codes.get(dtype)
@@ -963,12 +972,12 @@ def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, stream=None):
     dtype, dev = x.dtype, x.device
     code = E.code(dtype)
     px, ldx = _rows(x, "x", dtype, M, C)
-    q = E.empty((M, C), dtype=E.int8, device=dev)
-    scale = E.empty((M,), dtype=E.float32, device=dev)
+    q = E.mat(M, C, E.int8, dev)
+    scale = E.vec(M, E.float32, dev)
     pr, ldr, total, pt = None, 0, None, None
     if residual is not None:
         pr, ldr = _rows(residual, "residual", dtype, M, C)
-        total = E.empty((M, C), dtype=dtype, device=dev)
+        total = E.mat(M, C, dtype, dev)
         pt = total.data_ptr()
     rc = E.norm(px, ldx, pr, ldr, _vec(weight, "weight", C, E.float32), M, C, code, eps, pt, C,
                 q.data_ptr(), C, scale.data_ptr(), E.stream(x, stream))
@@ -983,8 +992,8 @@ def quant_q8(x, stream=None):
     M, C = _two_axes(x, "x")
     code = E.code(x.dtype)
     px, ldx = _rows(x, "x", x.dtype, M, C)
-    q = E.empty((M, C), dtype=E.int8, device=x.device)
-    scale = E.empty((M,), dtype=E.float32, device=x.device)
+    q = E.mat(M, C, E.int8, x.device)
+    scale = E.vec(M, E.float32, x.device)
     rc = E.quant(px, ldx, M, C, code, q.data_ptr(), C, scale.data_ptr(), E.stream(x, stream))
     if rc:
         _check(rc)
@@ -999,7 +1008,7 @@ def dequant_q8(q, scale, dtype=None, stream=None):
     M, C = _two_axes(q, "q")
     code = E.code(dtype)
     pq, ldq = _rows(q, "q", E.int8, M, C)
-    y = E.empty((M, C), dtype=dtype, device=q.device)
+    y = E.mat(M, C, dtype, q.device)
     rc = E.dequant(pq, ldq, _vec(scale, "scale", M, E.float32), M, C, code, y.data_ptr(), C,
                    E.stream(q, stream))
     if rc:
@@ -1019,9 +1028,9 @@ def linear_q8(a, a_scale, w, w_scale, bias=None, act: str = "none", dtype=None, 
         raise ValueError(f"act must be one of {sorted(ACT)}, got {act!r}")
     pa, lda = _rows(a, "a", E.int8, M, K)
     pw, ldw = _rows(w, "w", E.int8, N, K)
-    y = E.empty((M, N), dtype=dtype, device=a.device)
+    y = E.mat(M, N, dtype, a.device)
     need = E.linear_ws(M, N, K)
-    ws = E.empty((need,), dtype=E.uint8, device=a.device) if need else None
+    ws = E.vec(need, E.uint8, a.device) if need else None
     rc = E.linear(pa, lda, _vec(a_scale, "a_scale", M, E.float32), pw, ldw,
                   _vec(w_scale, "w_scale", N, E.float32),
                   None if bias is None else _vec(bias, "bias", N, E.float32), M, N, K, act_code,
@@ -1106,9 +1115,9 @@ def kv_read_q8(cache: KvCacheQ8, table, cu, lens, total: int, max_rows: Optional
     E = _q8()
     dtype = E.float32 if dtype is None else dtype
     code = E.code(dtype)
-    shape, dev = (total, cache.heads, cache.dim), cache.k.device
-    k = E.empty(shape, dtype=dtype, device=dev)
-    v = E.empty(shape, dtype=dtype, device=dev)
+    dev = cache.k.device
+    k = E.heads(total, cache.heads, cache.dim, dtype, dev)
+    v = E.heads(total, cache.heads, cache.dim, dtype, dev)
     rows = _ragged(E, table, cu, lens, total, max_rows)
     rc = E.read(cache.ref, ctypes.addressof(rows), code, k.data_ptr(), v.data_ptr(),
                 E.stream(cache.k, stream))
@@ -1133,10 +1142,10 @@ def attn_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = None,
     pr = ctypes.addressof(rows)
     if max_len is None:
         max_len = rows.table_cols * cache.page
-    out = E.empty((total, heads, dim), dtype=dtype, device=dev)
-    lse = E.empty((total, heads), dtype=E.float32, device=dev) if return_lse else None
+    out = E.heads(total, heads, dim, dtype, dev)
+    lse = E.mat(total, heads, E.float32, dev) if return_lse else None
     need = E.attn_ws(cache.ref, pr, heads, code, max_len, window)
-    ws = E.empty((need,), dtype=E.uint8, device=dev) if need else None
+    ws = E.vec(need, E.uint8, dev) if need else None
     rc = E.attn(pq, tok, head, heads, code, cache.ref, pr,
                 None if first is None else _vec(first, "first", rows.seqs, E.int32), max_len,
                 dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
