@@ -40,11 +40,13 @@ __device__ inline float scale_of(unsigned amax_bits) {
                                  : __uint_as_float(amax_bits) / 127.0f;
 }
 
-// The stored value nearest x / scale (ties to even, the division correctly
-// rounded), for |x| <= 127 scale; 0 where the scale is 0 or NaN.  The
-// quotient is x times the reciprocal, corrected by its own remainder (exact
-// in one fmaf); scales so small or large that reciprocal or remainder would
-// leave float32's normal range take the division itself.
+// x / scale, correctly rounded, for x in the row that the scale was taken
+// from; 0 where the scale is 0 or NaN.  The quotient is x times the
+// reciprocal, corrected by its own remainder (exact in one fmaf); scales so
+// small or large that reciprocal or remainder would leave float32's normal
+// range take the division itself.  A scale of a few of the smallest
+// subnormals can be a third below its row's maximum / 127: quotients past
+// 127 are held there.
 struct Quantiser {
     float scale, inv;
     bool plain;
@@ -56,7 +58,7 @@ struct Quantiser {
             const float r = x * inv;
             return fmaf(fmaf(-r, scale, x), inv, r);
         }
-        return scale > 0.0f ? x / scale : 0.0f;
+        return scale > 0.0f ? fminf(fmaxf(x / scale, -127.0f), 127.0f) : 0.0f;
     }
 };
 

@@ -129,6 +129,42 @@ def test_norm_rows_zero_and_non_finite(C):
         assert np.all(np.abs(got[keep] - rs[keep]) <= (C / 256 + 24) * U * np.abs(rs[keep]))
 
 
+@pytest.mark.parametrize("C", [3, 64, 1537, 33001])
+def test_rows_smallest_scales(C):
+    """Scales of a few of float32's smallest steps, rounded by up to a third:
+    values past 127 of them stay at 127."""
+    from bigvgan_waveform_decoder_amd import avae
+    announce(f"quant_q8 smallest scales C={C}")
+    rng = np.random.default_rng(C)
+    tops = np.array([1, 63, 64, 127, 128, 190, 191, 317, 1000, 20000])
+    x = rng.integers(-tops[:, None], tops[:, None] + 1, size=(len(tops), C))
+    x[:, 0], x[:, -1] = tops, -tops
+    x = (x * 2.0 ** -149).astype(np.float32)
+    assert np.array_equal(x.astype(np.float64)[:, 0], tops * 2.0 ** -149)
+    rq, rs, _ = R.rows_q8(x)
+    q, s = avae.quant_q8(_dev(x))
+    assert np.array_equal(_np(s).astype(np.float64), rs) and np.array_equal(_np(q), rq)
+    rq, _, _ = R.rows_q8(x, np.ones(C, np.float32))
+    assert np.array_equal(_np(avae.rms_norm_q8(_dev(x), _t().ones(C, device="cuda"))[0]), rq)
+
+
+@pytest.mark.parametrize("dim", [64, 256])
+def test_cache_smallest_scales(dim):
+    announce(f"kv_write_q8 smallest scales dim {dim}")
+    new, lens, page, heads = [256, 9], [256, 40], 256, 2
+    c = Cache(11, lens, heads, dim, page)
+    c.ks[c.table[1, 0]] = c.vs[c.table[1, 0]] = 2.0 ** -149
+    cu = _cu(new)
+    rng = np.random.default_rng(dim)
+    k, v = ((rng.integers(-top, top + 1, size=(cu[-1], heads, dim)) * 2.0 ** -149)
+            .astype(np.float32) for top in (190, 315))
+    dev = c.upload()
+    c.avae.kv_write_q8(dev, _dev(k), _dev(v), _dev(c.table), _dev(cu), _dev(c.lens))
+    R.kv_write(c.k8, c.ks, k, c.table, cu, lens, c.n, page)
+    R.kv_write(c.v8, c.vs, v, c.table, cu, lens, c.n, page)
+    assert c.same()
+
+
 def test_rows_none():
     from bigvgan_waveform_decoder_amd import avae
     torch = _t()
