@@ -2,12 +2,12 @@
 // read back.
 //
 // A page holds P tokens of every head, [head][token][dim], and one scale for
-// each head.  A page that gets its first token takes max|x| / 127 of its new
-// tokens as its scale.  One that holds tokens already keeps its scale if the
-// new tokens fit it; else it grows to theirs and the held values move to the
-// new range, q' = rint(q * old / new).  So writing the same tokens again
-// changes nothing, and one workgroup owns each (page, head): no atomics, and
-// the result does not depend on the order of the workgroups.
+// each head.  A page that gets its first token takes max|x| * (1 / 127) of
+// its new tokens as its scale.  One that holds tokens already keeps its scale
+// if the new tokens fit it; else it grows to theirs and the held values move
+// to the new range, q' = rint(q * old / new).  So writing the same tokens
+// again changes nothing, and one workgroup owns each (page, head): no
+// atomics, and the result does not depend on the order of the workgroups.
 //
 // HBM-bound: three ragged float32 prompts, 13600 tokens of 16 heads of 64,
 // take 25 us to write and 25 to read back (5.6 TB/s each); 64 appended

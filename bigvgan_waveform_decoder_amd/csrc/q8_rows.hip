@@ -1,7 +1,7 @@
 // Rows in 8 bits with one float32 scale each: root-mean-square norm with the
 // residual's addition, the plain row quantiser, and the read-back.
 //
-//   h = x + residual,  v = h * weight,  s = max|v| / 127,  q = rint(v / s),
+//   h = x + residual,  v = h * weight,  s = max|v| * (1 / 127),  q = rint(v / s),
 //   scale = s / sqrt(mean(h^2) + eps)
 //
 // The 8-bit values do not depend on the statistics (the row's factor

@@ -517,11 +517,12 @@ enum avae_act { AVAE_ACT_NONE = 0, AVAE_ACT_SILU = 1 };
  * Root-mean-square norm with the residual's addition and an 8-bit output:
  *   h = x + residual (x alone if residual is NULL), kept in float32;
  *   sum = h rounded to dtype (given exactly when residual is);
- *   v = h * weight;  s = max_c |v| / 127;  q = rint(v / s), ties to even;
+ *   v = h * weight;  s = max_c |v| * (1 / 127);
+ *   q = rint(v / s), ties to even, in [-127, 127];
  *   scale = s / sqrt(mean_c(h^2) + eps):
- * q * scale is the normed row.  A row of zeros (or one whose s underflows)
- * has q = 0 and scale = 0; a row whose v holds a NaN or an infinity has
- * q = 0 and scale = NaN.
+ * 1 / 127 is float32's; q * scale is the normed row.  A row of zeros (or one
+ * whose s underflows) has q = 0 and scale = 0; a row whose v holds a NaN or
+ * an infinity has q = 0 and scale = NaN.
  *   x, residual, sum: [M, C] at row strides ldx, ldr, ldsum; sum must
  *   overlap neither.  weight: [C] float32.  q: [M, C] 8-bit at ldq.
  *   scale: [M] float32.
@@ -601,8 +602,9 @@ typedef struct avae_ragged {
 /*
  * Quantise new keys and values as they are written.  For each page and head,
  * with new tokens x: if the page held no token of the sequence, its scale
- * becomes max|x| / 127; else it becomes the larger of that and what it was,
- * and where it grew the held values move to it, q' = rint(q * old / new).
+ * becomes max|x| * (1 / 127) as above; else it becomes the larger of that
+ * and what it was, and where it grew the held values move to it,
+ * q' = rint(q * old / new).
  * Then q = rint(x / scale), ties to even.  Writing the same tokens again
  * changes nothing.  A NaN or an infinity among the new tokens makes that
  * page's scale for that head NaN, and it stays NaN until the page is written

@@ -7,9 +7,9 @@ F32 = np.float32
 
 
 def scale_of(amax):
-    """amax / 127 in float32; NaN where amax is not finite."""
+    """amax times float32's 1 / 127; NaN where amax is not finite."""
     amax = np.asarray(amax, F32)
-    return np.where(np.isfinite(amax), amax / F32(127), F32(np.nan)).astype(F32)
+    return np.where(np.isfinite(amax), amax * (F32(1) / F32(127)), F32(np.nan)).astype(F32)
 
 
 def quantise(x, scale):

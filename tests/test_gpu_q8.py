@@ -165,6 +165,21 @@ def test_cache_smallest_scales(dim):
     assert c.same()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_rows_are_torchs_own(dtype):
+    """Values and scales are to the bit what the same steps written in torch
+    give on the device, so rows may come from either."""
+    from bigvgan_waveform_decoder_amd import avae
+    torch = _t()
+    announce(f"quant_q8 against torch's steps {dtype}")
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn((20011, 257), device="cuda", generator=gen).to(_dtype(dtype))
+    q, s = avae.quant_q8(x)
+    scale = x.float().abs().amax(1) / 127
+    assert torch.equal(s, scale)
+    assert torch.equal(q.float(), (x.float() / scale[:, None]).round())
+
+
 def test_rows_none():
     from bigvgan_waveform_decoder_amd import avae
     torch = _t()
