@@ -779,6 +779,14 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
 
 constexpr int kMaxSplits = 4224;  // over what the cut below can ask for
 
+// The factor of a chunk with maximum pm and sum pl where the row's maximum is
+// `at`.  A chunk without keys has written nothing else than pl = 0; a NaN sum
+// stays NaN whatever the maximum (which passes NaN scores by).
+__device__ inline float chunk_weight(float pm, float pl, float at) {
+    if (pl != pl) return pl;
+    return pl == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(pm - at);
+}
+
 // Joins the chunks of one output row: first their weights, then the weighted
 // sum, a thread for four dims and the chunks dealt to the workgroup's lanes.
 template <typename T, int D>
@@ -804,9 +812,7 @@ __global__ __launch_bounds__(512) void attn_q8_join_kernel(AttnQ8 a, int splits,
     const float at = m == neg_inf() ? 0.0f : m;
     float l = 0.0f;
     for (int s = threadIdx.x; s < splits; s += 512) {
-        const float pm = s_by[s], pl = pr[(long long)s * (D + 4) + 1];
-        // a chunk without keys has written nothing else
-        const float by = pm == neg_inf() && pl == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(pm - at);
+        const float pl = pr[(long long)s * (D + 4) + 1], by = chunk_weight(s_by[s], pl, at);
         s_by[s] = by;
         l += by == 0.0f ? 0.0f : by * pl;
     }
@@ -856,8 +862,7 @@ __global__ __launch_bounds__(256) void attn_q8_join_few_kernel(AttnQ8 a, int row
     float top = m;
     for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
     const float at = top == neg_inf() ? 0.0f : top;
-    // a chunk without keys has written nothing else
-    const float by = m == neg_inf() && l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - at);
+    const float by = chunk_weight(m, l, at);
     l = wave_sum(by == 0.0f ? 0.0f : by * l);
     const int col = lane % COLS;
     f4 o = {};

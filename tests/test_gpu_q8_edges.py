@@ -1,0 +1,64 @@
+"""The 8-bit serving operators where keys are split, ranges are wide, calls are
+padded and streams are mixed, against the plain numpy forms."""
+import numpy as np
+import pytest
+
+from tests import q8_reference as R
+from tests.gpu_util import announce
+from tests.test_gpu_q8 import ROUND, U, Cache, _cu, _dev, _dtype, _np, _t, _typed
+
+pytestmark = pytest.mark.gpu
+
+
+def _attend(c, new, qf, dtype, causal=True, window=0, first=None, **kw):
+    """(out, lse, reference out, reference lse, tolerance) of float64 queries."""
+    cu = _cu(new)
+    dq, qf = _typed(qf, dtype)
+    out, lse = c.avae.attn_q8(dq, c.upload(), _dev(c.table), _dev(cu), _dev(c.lens), causal=causal,
+                              window=window, first=None if first is None else _dev(first),
+                              return_lse=True, **kw)
+    with np.errstate(invalid="ignore"):
+        ref, rlse, weight, size = R.attention(qf, c.k8, c.ks, c.v8, c.vs, c.table, cu, list(c.lens),
+                                              c.page, c.dim ** -0.5, causal, window, first)
+    # Score: dim float32 additions and a few roundings, 22 bits of a float32
+    # query; probabilities: the score's error, their own rounding (11 or 22
+    # bits), the sums over the keys; float16's smallest step is 2^-40 of the
+    # row's largest value scale, which is at most the largest of the call.
+    length = max(c.lens)
+    ds = (c.dim + 16) * U * size + (2.0 ** -21 * size if dtype == "f32" else 0)
+    dp = 2 * np.expm1(ds) + (length / 8 + 64) * U + (2.0 ** -21 if dtype == "f32" else 2.0 ** -11)
+    rel, step = ROUND[dtype]
+    tol = dp[:, :, None] * weight + rel * np.abs(ref) + step
+    return _np(out), _np(lse), ref, rlse, tol
+
+
+# new, lengths, heads, cache heads, dim: few and many rows, each with either join
+SPLIT = [([1], [2400], 4, 2, 64), ([1], [2400], 4, 2, 128), ([2], [1300], 2, 1, 256),
+         ([1] * 32, [600] * 31 + [410], 64, 2, 64), ([1] * 32, [500] * 32, 64, 2, 128),
+         ([100], [1500], 8, 2, 64), ([70], [1100], 4, 2, 128), ([260], [1300], 8, 1, 64),
+         ([260], [1400], 8, 1, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,lens,heads,kv_heads,dim", SPLIT)
+@pytest.mark.parametrize("what", ["query", "k page", "v page", "k pages", "v pages"])
+def test_nan_stays_where_keys_are_split(what, new, lens, heads, kv_heads, dim, dtype):
+    """A NaN query row, a NaN page as long as a chunk and caches of nothing
+    else: exactly the rows that see one are NaN, however the keys are cut."""
+    announce(f"attn_q8 NaN {what}, split keys {new[:3]} {lens[:3]} {heads}/{kv_heads} dim {dim} {dtype}")
+    c = Cache(50, lens, kv_heads, dim, 128)
+    c.poison_unused()
+    rng = np.random.default_rng(3)
+    q = rng.normal(size=(sum(new), heads, dim)) * 2
+    if what == "query":
+        q[0, heads - 1, 5] = np.nan
+    scales = c.vs if what[0] == "v" else c.ks
+    if "page" in what:
+        scales[c.table[0, 2 if what.endswith("page") else slice(0, -(-lens[0] // 128))],
+               kv_heads - 1] = np.nan
+    out, lse, ref, rlse, tol = _attend(c, new, q, dtype)
+    bad = np.isnan(ref).any(2)
+    assert bad.any() and np.array_equal(np.isnan(ref).all(2), bad)
+    assert np.array_equal(np.isnan(out), np.isnan(ref)) and np.array_equal(np.isnan(lse), bad)
+    assert np.all(np.abs(out - ref)[~bad] <= tol[~bad])
+    assert np.all(np.abs(lse - rlse)[~bad] <= 1e-3)
