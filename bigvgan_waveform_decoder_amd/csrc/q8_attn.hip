@@ -867,8 +867,9 @@ __global__ __launch_bounds__(256) void attn_q8_join_few_kernel(AttnQ8 a, int row
     const int col = lane % COLS;
     f4 o = {};
     for (int s0 = 0; s0 < splits; s0 += LANES) {
+        // (every lane takes part in the exchange, those past the last chunk too)
         const int s = s0 + lane / COLS;
-        const float w = s < splits ? __shfl(by, s) : 0.0f;
+        const float from = __shfl(by, min(s, splits - 1)), w = s < splits ? from : 0.0f;
         if (w != 0.0f)
             o += w * *reinterpret_cast<const f4*>(pr + (long long)s * (D + 4) + 4 + 4 * col);
     }

@@ -62,3 +62,25 @@ def test_nan_stays_where_keys_are_split(what, new, lens, heads, kv_heads, dim, d
     assert np.array_equal(np.isnan(out), np.isnan(ref)) and np.array_equal(np.isnan(lse), bad)
     assert np.all(np.abs(out - ref)[~bad] <= tol[~bad])
     assert np.all(np.abs(lse - rlse)[~bad] <= 1e-3)
+
+
+# heads of 64, 128 and 256 dims: 4, 2 and 1 chunks a wave and step
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv_heads,dim,total", [(4, 4, 64, 512), (4, 2, 128, 600),
+                                                      (2, 1, 256, 1100)])
+@pytest.mark.parametrize("length", [300, 2050, 2600, 4170, 5249, 8190])
+def test_packed_rows_longer_than_the_sequences(length, heads, kv_heads, dim, total, dtype):
+    """Packed tensors with rows that belong to no sequence, which choose the
+    join for many rows: any number of chunks, odd ones among them."""
+    announce(f"attn_q8 padded total {total}, {length} keys {heads}/{kv_heads} dim {dim} {dtype}")
+    c = Cache(51, [length], kv_heads, dim, 64)
+    c.poison_unused()
+    rng = np.random.default_rng(5)
+    q = rng.normal(size=(total, heads, dim)) * 2
+    dq, _ = _typed(q, dtype)
+    got, glse = c.avae.attn_q8(dq, c.upload(), _dev(c.table), _dev(_cu([1])), _dev(c.lens), max_q=1,
+                               return_lse=True)
+    out, lse, ref, rlse, tol = _attend(c, [1], q[:1], dtype)  # the row alone: joined otherwise
+    for o, l in ((out, lse), (_np(got)[:1], _np(glse)[:1])):
+        assert np.all(np.abs(o - ref) <= tol)
+        assert np.all(np.abs(l - rlse) <= 1e-3)
