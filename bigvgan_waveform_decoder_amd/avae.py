@@ -878,6 +878,11 @@ class BweDecoder:
 # These calls take a few microseconds on the device, so what the binding does
 # for each of them counts: names are looked up once, and a tensor is asked
 # for its properties once.
+#
+# A call runs on the current stream, or on `stream` (a torch stream): then all
+# of it does, what it allocates included, so that no memory of the current
+# stream is written or given back while the other one still works.  Outputs
+# belong to that stream, as with torch's own operators under it.
 
 ACT = {"none": 0, "silu": 1}
 
@@ -914,10 +919,9 @@ class _Env:
             raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
         return code
 
-    def stream(self, t, stream):
-        """The raw stream to launch on: the given one, or the current one of
-        the tensor's device."""
-        return self.raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+    def stream(self, t):
+        """The raw stream to launch on: the current one of the tensor's device."""
+        return self.raw_stream(t.get_device())
 
 
 _env: Optional[_Env] = None
@@ -967,6 +971,9 @@ def _two_axes(t, name: str):
 def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, stream=None):
     """avae_rms_norm_q8: x [M, C] (+ residual) -> (q [M, C] int8, scale [M],
     the sum in x's dtype or None)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return rms_norm_q8(x, weight, eps, residual)
     E = _q8()
     M, C = _two_axes(x, "x")
     dtype, dev = x.dtype, x.device
@@ -980,7 +987,7 @@ def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, stream=None):
         total = E.mat(M, C, dtype, dev)
         pt = total.data_ptr()
     rc = E.norm(px, ldx, pr, ldr, _vec(weight, "weight", C, E.float32), M, C, code, eps, pt, C,
-                q.data_ptr(), C, scale.data_ptr(), E.stream(x, stream))
+                q.data_ptr(), C, scale.data_ptr(), E.stream(x))
     if rc:
         _check(rc)
     return q, scale, total
@@ -988,13 +995,16 @@ def rms_norm_q8(x, weight, eps: float = 1e-6, residual=None, stream=None):
 
 def quant_q8(x, stream=None):
     """avae_quant_q8: x [M, C] -> (q [M, C] int8, scale [M])."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return quant_q8(x)
     E = _q8()
     M, C = _two_axes(x, "x")
     code = E.code(x.dtype)
     px, ldx = _rows(x, "x", x.dtype, M, C)
     q = E.mat(M, C, E.int8, x.device)
     scale = E.vec(M, E.float32, x.device)
-    rc = E.quant(px, ldx, M, C, code, q.data_ptr(), C, scale.data_ptr(), E.stream(x, stream))
+    rc = E.quant(px, ldx, M, C, code, q.data_ptr(), C, scale.data_ptr(), E.stream(x))
     if rc:
         _check(rc)
     return q, scale
@@ -1003,6 +1013,9 @@ def quant_q8(x, stream=None):
 def dequant_q8(q, scale, dtype=None, stream=None):
     """avae_dequant_q8: q [M, C] int8 with a scale a row -> [M, C] of dtype
     (float32 if none is given)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return dequant_q8(q, scale, dtype)
     E = _q8()
     dtype = E.float32 if dtype is None else dtype
     M, C = _two_axes(q, "q")
@@ -1010,7 +1023,7 @@ def dequant_q8(q, scale, dtype=None, stream=None):
     pq, ldq = _rows(q, "q", E.int8, M, C)
     y = E.mat(M, C, dtype, q.device)
     rc = E.dequant(pq, ldq, _vec(scale, "scale", M, E.float32), M, C, code, y.data_ptr(), C,
-                   E.stream(q, stream))
+                   E.stream(q))
     if rc:
         _check(rc)
     return y
@@ -1019,6 +1032,9 @@ def dequant_q8(q, scale, dtype=None, stream=None):
 def linear_q8(a, a_scale, w, w_scale, bias=None, act: str = "none", dtype=None, stream=None):
     """avae_linear_q8: a [M, K] int8, w [N, K] int8 with a scale a row each
     -> [M, N] of dtype (float32 if none is given)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return linear_q8(a, a_scale, w, w_scale, bias, act, dtype)
     E = _q8()
     dtype = E.float32 if dtype is None else dtype
     M, K = _two_axes(a, "a")
@@ -1035,7 +1051,7 @@ def linear_q8(a, a_scale, w, w_scale, bias=None, act: str = "none", dtype=None, 
                   _vec(w_scale, "w_scale", N, E.float32),
                   None if bias is None else _vec(bias, "bias", N, E.float32), M, N, K, act_code,
                   code, y.data_ptr(), N, None if ws is None else ws.data_ptr(), need,
-                  E.stream(a, stream))
+                  E.stream(a))
     if rc:
         _check(rc)
     return y
@@ -1097,13 +1113,16 @@ def kv_write_q8(cache: KvCacheQ8, k, v, table, cu, lens, max_new: Optional[int] 
                 stream=None):
     """avae_kv_write_q8: k, v [tokens, heads, dim] into the cache's pages.
     max_new: at least the most rows of one sequence (all of them if not given)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return kv_write_q8(cache, k, v, table, cu, lens, max_new)
     E = _q8()
     total = k.shape[0]
     if v.dtype != k.dtype or v.shape[0] != total:
         raise ValueError("k and v must have one dtype and as many tokens")
     rows = _ragged(E, table, cu, lens, total, max_new)
     rc = E.write(*_heads(k, "k", cache.heads, cache.dim), *_heads(v, "v", cache.heads, cache.dim),
-                 E.code(k.dtype), cache.ref, ctypes.addressof(rows), E.stream(k, stream))
+                 E.code(k.dtype), cache.ref, ctypes.addressof(rows), E.stream(k))
     if rc:
         _check(rc)
 
@@ -1112,6 +1131,9 @@ def kv_read_q8(cache: KvCacheQ8, table, cu, lens, total: int, max_rows: Optional
                dtype=None, stream=None):
     """avae_kv_read_q8: the sequences' last tokens, `total` of them, as cu
     says -> k, v [total, heads, dim] of dtype (float32 if none is given)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return kv_read_q8(cache, table, cu, lens, total, max_rows, dtype)
     E = _q8()
     dtype = E.float32 if dtype is None else dtype
     code = E.code(dtype)
@@ -1120,7 +1142,7 @@ def kv_read_q8(cache: KvCacheQ8, table, cu, lens, total: int, max_rows: Optional
     v = E.heads(total, cache.heads, cache.dim, dtype, dev)
     rows = _ragged(E, table, cu, lens, total, max_rows)
     rc = E.read(cache.ref, ctypes.addressof(rows), code, k.data_ptr(), v.data_ptr(),
-                E.stream(cache.k, stream))
+                E.stream(cache.k))
     if rc:
         _check(rc)
     return k, v
@@ -1133,6 +1155,10 @@ def attn_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = None,
     (and lse [tokens, q_heads] float32 if asked for).  max_q: at least the most
     rows of one sequence; max_len: at least the longest sequence (the table's
     tokens if not given); scale: 1 / sqrt(dim) if not given."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return attn_q8(q, cache, table, cu, lens, max_q, max_len, scale, causal, window, first,
+                           return_lse)
     E = _q8()
     dim, dtype, dev = cache.dim, q.dtype, q.device
     code = E.code(dtype)
@@ -1150,7 +1176,7 @@ def attn_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = None,
                 None if first is None else _vec(first, "first", rows.seqs, E.int32), max_len,
                 dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
                 out.data_ptr(), None if lse is None else lse.data_ptr(),
-                None if ws is None else ws.data_ptr(), need, E.stream(q, stream))
+                None if ws is None else ws.data_ptr(), need, E.stream(q))
     if rc:
         _check(rc)
     return (out, lse) if return_lse else out

@@ -84,3 +84,59 @@ def test_packed_rows_longer_than_the_sequences(length, heads, kv_heads, dim, tot
     for o, l in ((out, lse), (_np(got)[:1], _np(glse)[:1])):
         assert np.all(np.abs(o - ref) <= tol)
         assert np.all(np.abs(l - rlse) <= 1e-3)
+
+
+def test_stream_argument():
+    """Calls on a stream other than the current one, which has work ahead of
+    them: what the current stream allocates right after the call returns is
+    its own, whether the outputs are kept or dropped."""
+    from bigvgan_waveform_decoder_amd import avae
+    torch = _t()
+    rng = np.random.default_rng(12)
+    c = Cache(52, [9001], 2, 64, 16)
+    dev = c.upload()
+    one, back = _dev(_cu([1])), _dev(_cu([800]))
+    table, lens = _dev(c.table), _dev(c.lens)
+    x, w = _dev(rng.normal(size=(1000, 500)).astype(np.float32)), _dev(np.ones(500, np.float32))
+    a, sa = avae.quant_q8(_dev(rng.normal(size=(1000, 77)).astype(np.float32)))
+    b, sb = avae.quant_q8(_dev(rng.normal(size=(900, 77)).astype(np.float32)))
+    q = _dev(rng.normal(size=(1, 8, 64)).astype(np.float32))
+    kv = _dev(rng.normal(size=(1, 2, 64)).astype(np.float32))
+    assert avae.lib().avae_linear_q8_workspace_bytes(1000, 900, 77) > 0
+
+    def write(s):
+        avae.kv_write_q8(dev, kv, kv, table, one, lens, stream=s)
+        return avae.kv_read_q8(dev, table, one, lens, 1, stream=s)
+
+    calls = {
+        "rms_norm_q8": lambda s: avae.rms_norm_q8(x, w, residual=x, stream=s),
+        "quant_q8": lambda s: avae.quant_q8(x, stream=s),
+        "dequant_q8": lambda s: avae.dequant_q8(a, sa, stream=s),
+        "linear_q8": lambda s: avae.linear_q8(a, sa, b, sb, stream=s),
+        "kv_write_q8": write,
+        "kv_read_q8": lambda s: avae.kv_read_q8(dev, table, back, lens, 800, stream=s),
+        "attn_q8": lambda s: avae.attn_q8(q, dev, table, one, lens, return_lse=True, stream=s)}
+    side = torch.cuda.Stream()
+    busy = torch.zeros(1 << 28, device="cuda")
+    # workspaces and outputs of these calls, in bytes
+    sizes = [avae.lib().avae_linear_q8_workspace_bytes(1000, 900, 77), 1000 * 900 * 4, 1000 * 500 * 4,
+             1000 * 500, 1000 * 77 * 4, 4000, 800 * 128 * 4, 512, 2048]
+    sizes += [8 * n * 68 * 4 for n in range(60, 80)]  # parts of the attention, whatever their number
+
+    for name, call in calls.items():
+        announce(f"{name} on a stream of its own")
+        as_list = lambda y: list(y) if isinstance(y, tuple) else [y]
+        want = [t.clone() for t in as_list(call(None))]
+        torch.cuda.synchronize()
+        for keep in (True, False):
+            with torch.cuda.stream(side):
+                for _ in range(10):
+                    busy.add_(1)
+            out = as_list(call(side))
+            if not keep:
+                del out
+            marks = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for n in 2 * sizes]
+            torch.cuda.synchronize()
+            assert all(bool((m == 0x55).all()) for m in marks)
+            if keep:
+                assert all(torch.equal(g, t) for g, t in zip(out, want))
