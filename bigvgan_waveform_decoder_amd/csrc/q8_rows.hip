@@ -25,6 +25,39 @@ namespace {
 
 using namespace q8;
 
+// Whether float32 holds a finite row's sum of squares: it may pass the
+// largest number (|h| above 1.8e19), or its squares fall below the normal
+// range where eps is too small to hide it.
+__device__ inline bool squares_hold(float sq, float eps) {
+    return sq < __uint_as_float(kInfBits) && (sq >= 0x1p-80f || eps >= 0x1p-100f);
+}
+
+// The scale of a normed row, for a row of zeros 0 whatever eps is.
+__device__ inline float normed_scale(float s, float sq, int C, float eps) {
+    return s == 0.0f ? 0.0f : s * (1.0f / sqrtf(sq / (float)C + eps));
+}
+
+// The same for the rare rows whose squares float32 does not hold: read again,
+// summed in 64 bits by the row's THREADS threads; thread 0 has the result.
+template <typename T, bool RES, int THREADS>
+__device__ float normed_scale_wide(const T* x, const T* res, int C, int tid, float s, float eps,
+                                   double* s_part) {
+    double sq = 0.0;
+    for (int c = tid; c < C; c += THREADS) {
+        float h = (float)x[c];
+        if (RES) h += (float)res[c];
+        sq += (double)h * (double)h;
+    }
+    for (int o = 32; o > 0; o >>= 1) sq += __shfl_xor(sq, o);
+    if (THREADS > 64) {
+        if ((tid & 63) == 0) s_part[tid >> 6] = sq;
+        __syncthreads();
+        sq = 0.0;
+        for (int i = 0; i < THREADS / 64; ++i) sq += s_part[i];
+    }
+    return (float)((double)s / sqrt(sq / C + (double)eps));
+}
+
 // One row a group of THREADS threads (64 of a workgroup of 256, or a whole
 // workgroup of 256 or 1024), its values held in registers between the pass
 // that finds the maximum and the one that rounds: 8 HELD a thread.
@@ -102,7 +135,7 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rows_q8_kernel(
         }
     }
     const float s = scale_of(top);
-    if (tid == 0) scale[row] = NORM ? s * (1.0f / sqrtf(sq / (float)C + eps)) : s;
+    if (tid == 0) scale[row] = NORM ? normed_scale(s, sq, C, eps) : s;
     const Quantiser quant(s);
 #pragma unroll
     for (int j = 0; j < HELD; ++j) {
@@ -114,6 +147,12 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void rows_q8_kernel(
             out[h] = to_bytes(quant.quotient(v[j][4 * h]), quant.quotient(v[j][4 * h + 1]),
                               quant.quotient(v[j][4 * h + 2]), quant.quotient(v[j][4 * h + 3]));
         store_bytes<8>(q + row * ldq + c, left, out);
+    }
+    if (NORM && s > 0.0f && !squares_hold(sq, eps)) {  // all of the row's threads or none
+        __shared__ double s_part[WAVES];
+        const float wide = normed_scale_wide<T, RES, THREADS>(
+            x + row * ldx, RES ? res + row * ldr : nullptr, C, tid, s, eps, s_part);
+        if (tid == 0) scale[row] = wide;
     }
 }
 
@@ -153,13 +192,18 @@ __global__ __launch_bounds__(1024) void long_rows_q8_kernel(
         sq += s_sq[i];
     }
     const float s = scale_of(top);
-    if (threadIdx.x == 0) scale[row] = NORM ? s * (1.0f / sqrtf(sq / (float)C + eps)) : s;
+    if (threadIdx.x == 0) scale[row] = NORM ? normed_scale(s, sq, C, eps) : s;
     const Quantiser quant(s);
     for (int c = threadIdx.x; c < C; c += 1024) {
         float h = (float)xr[c];
         if (RES) h += (float)rr[c];
         q[row * ldq + c] =
             (int8_t)to_bytes(quant.quotient(NORM ? h * w[c] : h), 0.0f, 0.0f, 0.0f);
+    }
+    if (NORM && s > 0.0f && !squares_hold(sq, eps)) {
+        __shared__ double s_part[16];
+        const float wide = normed_scale_wide<T, RES, 1024>(xr, rr, C, threadIdx.x, s, eps, s_part);
+        if (threadIdx.x == 0) scale[row] = wide;
     }
 }
 

@@ -521,8 +521,9 @@ enum avae_act { AVAE_ACT_NONE = 0, AVAE_ACT_SILU = 1 };
  *   q = rint(v / s), ties to even, in [-127, 127];
  *   scale = s / sqrt(mean_c(h^2) + eps):
  * 1 / 127 is float32's; q * scale is the normed row.  A row of zeros (or one
- * whose s underflows) has q = 0 and scale = 0; a row whose v holds a NaN or
- * an infinity has q = 0 and scale = NaN.
+ * whose s underflows) has q = 0 and scale = 0 whatever eps is; a row whose v
+ * holds a NaN or an infinity has q = 0 and scale = NaN.  The mean is taken in
+ * 64 bits for rows whose squares leave float32's range.
  *   x, residual, sum: [M, C] at row strides ldx, ldr, ldsum; sum must
  *   overlap neither.  weight: [C] float32.  q: [M, C] 8-bit at ldq.
  *   scale: [M] float32.

@@ -140,3 +140,28 @@ def test_stream_argument():
             assert all(bool((m == 0x55).all()) for m in marks)
             if keep:
                 assert all(torch.equal(g, t) for g, t in zip(out, want))
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-35, 1e-6])
+@pytest.mark.parametrize("C", [1, 5, 500, 1536, 9000, 33001])
+def test_norm_rows_scales_over_the_whole_range(C, eps):
+    """Rows of zeros, rows whose squares pass float32's largest number or fall
+    below its smallest, and ordinary ones beside them."""
+    from bigvgan_waveform_decoder_amd import avae
+    announce(f"rms_norm_q8 range C={C} eps={eps}")
+    rng = np.random.default_rng(C)
+    tops = [0, 1e-44, 3e-39, 1e-30, 1e-22, 1e-12, 1.0, 1e15, 1e19, 1e20, 1e30, 1e37]
+    x = rng.normal(size=(len(tops), C))
+    x = (x / np.abs(x).max(1, keepdims=True) * np.array(tops)[:, None]).astype(np.float32)
+    r = (x * rng.normal(size=x.shape) * 0.1).astype(np.float32)
+    w = (1 + 0.2 * rng.normal(size=C)).astype(np.float32)
+    for res in (None, r):
+        q, s, _ = avae.rms_norm_q8(_dev(x), _dev(w), eps=eps, residual=None if res is None else _dev(res))
+        with np.errstate(invalid="ignore"):
+            rq, rs, _ = R.rows_q8(x, w, res, float(np.float32(eps)))
+        rs[np.abs(rq).max(1) == 0] = 0
+        assert rs[0] == 0 and np.isfinite(rs).all()
+        got = _np(s).astype(np.float64)
+        assert np.array_equal(_np(q), rq)
+        # C/256 terms a lane and a few roundings; float32's smallest step
+        assert np.all(np.abs(got - rs) <= (C / 256 + 24) * U * rs + 2.0 ** -149), (got, rs)
