@@ -145,14 +145,15 @@ __device__ inline void load_stored(const int8_t* p, int left, float (&x)[N]) {
     }
 }
 
-// Rows cu[b] .. cu[b+1] of sequence b; false if it has none, or if the
-// offsets do not lie in the packed rows.
+// Rows cu[b] .. cu[b+1] of sequence b and its length (not below 0: then its
+// rows are tokens of no page); false if it has none, or if the offsets do not
+// lie in the packed rows.
 __device__ inline bool ragged_rows(const Ragged& r, int b, int& at, int& n, int& len) {
     at = r.cu[b];
     const int end = r.cu[b + 1];
-    len = r.lens[b];
+    len = max(r.lens[b], 0);
     n = end - at;
-    return at >= 0 && end > at && end <= r.total && len > 0;
+    return at >= 0 && end > at && end <= r.total;
 }
 
 // The page of a table's column, or -1 if there is none: a column outside the

@@ -213,10 +213,7 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
     const int split = blockIdx.x / all, in_all = blockIdx.x % all;
     const int b = in_all / pairs, tile = in_all % pairs / c.heads, head = in_all % c.heads;
     int cu0, n, len;
-    if (!ragged_rows(r, b, cu0, n, len)) {
-        if (cu0 < 0 || n <= 0 || cu0 + (long long)n > r.total) return;
-        len = 0;  // rows of a sequence without tokens see nothing
-    }
+    if (!ragged_rows(r, b, cu0, n, len)) return;
     const int group = a.q_heads / c.heads;
     if (tile * 16 >= n * group) return;
     if (pieces) {
@@ -470,10 +467,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
     const int head = pair % c.heads, b = pair / c.heads;
     const int split = blockIdx.x / pairs % splits, tile = tiles - 1 - blockIdx.x / pairs / splits;
     int cu0, n, len;
-    if (!ragged_rows(r, b, cu0, n, len)) {
-        if (cu0 < 0 || n <= 0 || cu0 + (long long)n > r.total) return;
-        len = 0;
-    }
+    if (!ragged_rows(r, b, cu0, n, len)) return;
     const int group = a.q_heads / c.heads, rows = n * group, r0 = tile * HEIGHT;
     if (r0 >= rows) return;
     // keys that any of the workgroup's rows sees; bounds grow with the row

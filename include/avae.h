@@ -613,7 +613,9 @@ typedef struct avae_ragged {
  *   k, v: [total, heads, dim] of dtype at token strides k_tok, v_tok and
  *   head strides k_head, v_head.
  * avae_kv_read_q8 reads rows back: k, v [total, heads, dim] contiguous, of
- *   dtype; the rows are the sequences' last tokens as `rows` says.
+ *   dtype; the rows are the sequences' last tokens as `rows` says (zeros for
+ *   those before a sequence's first token; rows of no sequence stay as they
+ *   were).
  * Errors: EINVAL, ESHAPE.
  */
 int avae_kv_write_q8(const void* k, long long k_tok, long long k_head, const void* v,

@@ -165,3 +165,34 @@ def test_norm_rows_scales_over_the_whole_range(C, eps):
         assert np.array_equal(_np(q), rq)
         # C/256 terms a lane and a few roundings; float32's smallest step
         assert np.all(np.abs(got - rs) <= (C / 256 + 24) * U * rs + 2.0 ** -149), (got, rs)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_cache_read_of_sequences_without_tokens(dtype):
+    """Rows of a sequence of length 0 (or below) are zeros, rows of none stay."""
+    import ctypes
+    from bigvgan_waveform_decoder_amd import avae
+    announce(f"kv_read_q8 lengths of 0 {dtype}")
+    torch = _t()
+    c = Cache(53, [20, 0, 40, 0], 2, 64, 16)
+    dev = c.upload()
+    c.lens[3] = -5
+    new = [20, 3, 2, 4]
+    table, cu, lens = _dev(c.table), _dev(_cu(new)), _dev(c.lens)
+    k, v = (torch.full((31, 2, 64), 7.0, dtype=_dtype(dtype), device="cuda") for _ in range(2))
+    rows = avae.avae_ragged(cu.data_ptr(), lens.data_ptr(), table.data_ptr(), c.table.shape[1],
+                            c.table.shape[1], 4, 31, 20)
+    assert avae.lib().avae_kv_read_q8(dev.ref, ctypes.byref(rows), {"f32": 0, "bf16": 1}[dtype],
+                                      k.data_ptr(), v.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream) == 0
+    before = _np(dev.k).copy(), _np(dev.k_scale).copy()
+    for got, q8, s in ((k, c.k8, c.ks), (v, c.v8, c.vs)):
+        want = R.kv_read(q8, s, c.table, _cu(new), [20, 0, 40, 0], 16)
+        want = torch.from_numpy(want).to(_dtype(dtype)).float().numpy()
+        assert (want[20:23] == 0).all() and (want[25:29] == 0).all() and (want[23:25] != 0).any()
+        assert np.array_equal(_np(got)[:29], want) and (_np(got)[29:] == 7).all()
+    # and a write of such rows changes nothing
+    x = torch.ones((29, 2, 64), device="cuda")
+    only = _dev(np.array([0, 0, 3, 3, 7], np.int32))
+    avae.kv_write_q8(dev, x, x, table, only, lens)
+    assert np.array_equal(_np(dev.k), before[0]) and np.array_equal(_np(dev.k_scale), before[1])
