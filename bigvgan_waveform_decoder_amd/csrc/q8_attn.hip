@@ -633,7 +633,9 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
     auto weigh = [&](const f16v& s, int u, float by, const Group& gr, h8& ph, h8& pl) {
         const float m_at = m == neg_inf() ? 0.0f : m;
         const float lift = fmaxf(gr.lg_vs + 15.0f - lg_run, -60.0f) - m_at;
-        const float drop = fminf(gr.vs * __builtin_amdgcn_exp2f(lg_run - 15.0f), 0x1p60f);
+        // (in two halves: the units of small value scales are below float32)
+        const float half = __builtin_amdgcn_exp2f(0.5f * (lg_run - 15.0f));
+        const float drop = fminf(gr.vs * half * half, 0x1p60f);
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -736,8 +738,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
     l += __shfl_xor(l, 32);
     if (!row.live) return;
     const long long out_row = (long long)row.tok * a.q_heads + row.q_head;
-    const float unit = __builtin_amdgcn_exp2f(lg_run - 15.0f);
-    const float by = splits > 1 ? unit : l == 0.0f ? 0.0f : unit / l;  // a NaN sum stays NaN
+    const float half = __builtin_amdgcn_exp2f(0.5f * (lg_run - 15.0f));  // of the units, as above
+    const float by = splits > 1 ? half : l == 0.0f ? 0.0f : half / l;  // a NaN sum stays NaN
     float* pr = part + (out_row * splits + split) * (D + 4);
     // dims 4 p .. 4 p + 3 are in rows p, D / 4 + p, D / 2 + p, 3 D / 4 + p of
     // the stacked output tiles
@@ -749,7 +751,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int at = e * (D / 4) + p8;
-                o[e] = acc[at / 32][at % 32 / 8 * 4 + i] * by;
+                o[e] = acc[at / 32][at % 32 / 8 * 4 + i] * by * half;
             }
             const int d = 4 * (p8 + 4 * g + i);
             if (splits > 1) {

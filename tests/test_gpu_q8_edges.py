@@ -196,3 +196,44 @@ def test_cache_read_of_sequences_without_tokens(dtype):
     only = _dev(np.array([0, 0, 3, 3, 7], np.int32))
     avae.kv_write_q8(dev, x, x, table, only, lens)
     assert np.array_equal(_np(dev.k), before[0]) and np.array_equal(_np(dev.k_scale), before[1])
+
+
+def _scaled_cache(seed, lens, heads, dim, page, low, high, zeros):
+    """Value scales 2^low .. 2^high, a page each; every fifth page of zeros if asked for."""
+    c = Cache(seed, lens, heads, dim, page)
+    c.poison_unused()
+    rng = np.random.default_rng(seed)
+    for b, t in enumerate(lens):
+        for col in range(-(-t // page)):
+            p = c.table[b, col]
+            c.vs[p] = np.exp2(rng.integers(low, high + 1)).astype(np.float32)
+            if zeros and col % 5 == 3:
+                c.vs[p], c.v8[p] = 0, 0
+    return c
+
+
+def _check_scaled(c, new, heads, dtype, q):
+    out, lse, ref, rlse, tol = _attend(c, new, q, dtype)
+    # float16's smallest step: 2^-40 of the largest value scale for each key;
+    # the smallest bfloat16 step of outputs near float32's own end
+    top = c.vs[c.table[c.table >= 0]].max()
+    tol = tol + 2.0 ** -40 * 127 * max(c.lens) * top + 2.0 ** -133
+    assert np.all(np.abs(out - ref) <= tol), (np.abs(out - ref) / tol).max()
+    assert np.all(np.abs(lse - rlse) <= 1e-3)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,dim", [(2, 64), (4, 128), (2, 256)])
+@pytest.mark.parametrize("new,lens", [([100, 70, 64, 40], [200, 200, 64, 130]), ([90], [1300])])
+def test_many_rows_over_small_and_distant_value_scales(new, lens, heads, dim, dtype):
+    """Value scales down to float32's smallest normal number, scales far apart,
+    pages of zeros: many rows, whole and split."""
+    rng = np.random.default_rng(9)
+    q = rng.normal(size=(sum(new), heads, dim))
+    q[0] *= 1e-30
+    q[1] *= 30
+    q[2] = 0
+    for low, high, zeros in ((-126, -126, False), (-125, -112, True), (-112, -90, False),
+                             (-20, 10, True), (60, 90, False)):
+        announce(f"attn_q8 many rows, value scales 2^{low}..2^{high} {new} {lens} dim {dim} {dtype}")
+        _check_scaled(_scaled_cache(61, lens, 2, dim, 16, low, high, zeros), new, heads, dtype, q)
