@@ -254,7 +254,9 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
     const float to_log2 = q.back * a.scale * kLog2e;
 
     f4 acc[DT] = {};
-    float m = neg_inf(), l = 0.0f, v_run = 0.0f;
+    // v_run: the largest value scale so far, the accumulated values' unit; at
+    // least float32's smallest normal number, which has a reciprocal
+    float m = neg_inf(), l = 0.0f, v_run = 0x1p-126f;
     for (int t0 = t_lo + 32 * wave; t0 < t_hi; t0 += 32 * kWaves) {
         f4 s[2];
         float vs[2];
@@ -321,7 +323,7 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
         const float m_at = m_new == neg_inf() ? 0.0f : m_new;
         // the largest value scale so far stands at 2^15
         const float v_new = fmaxf(v_run, fmaxf(vs[0], vs[1]));
-        const float inv = 1.0f / fmaxf(v_new, 1e-38f);
+        const float inv = 1.0f / v_new;
         float back = __builtin_amdgcn_exp2f(m - m_at);
         l *= back;
         back *= v_run * inv;
@@ -377,13 +379,13 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
         s_l[wave * 16 + n16] = l;
     }
     if (row.live) {
-        const float unit = v_run * (1.0f / 32768.0f);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int t = 0; t < DT; t += 4)
                 *reinterpret_cast<f4*>(s_out + (wave * 16 + n16) * LD + DT * (4 * g + i) + t) =
-                    (f4){acc[t][i], acc[t + 1][i], acc[t + 2][i], acc[t + 3][i]} * unit;
+                    (f4){acc[t][i], acc[t + 1][i], acc[t + 2][i], acc[t + 3][i]} *
+                    (1.0f / 32768.0f) * v_run;
     }
     __syncthreads();
     // each thread joins four dims of a row

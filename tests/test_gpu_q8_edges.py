@@ -237,3 +237,19 @@ def test_many_rows_over_small_and_distant_value_scales(new, lens, heads, dim, dt
                              (-20, 10, True), (60, 90, False)):
         announce(f"attn_q8 many rows, value scales 2^{low}..2^{high} {new} {lens} dim {dim} {dtype}")
         _check_scaled(_scaled_cache(61, lens, 2, dim, 16, low, high, zeros), new, heads, dtype, q)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,dim", [(2, 64), (4, 128), (2, 256)])
+@pytest.mark.parametrize("new,lens", [([1, 2, 8], [200, 64, 130]), ([3], [1300])])
+def test_few_rows_over_small_and_distant_value_scales(new, lens, heads, dim, dtype):
+    """The same with few rows, below float32's smallest normal number as well."""
+    rng = np.random.default_rng(9)
+    q = rng.normal(size=(sum(new), heads, dim))
+    q[0] *= 1e-30
+    q[1] *= 30
+    q[2] = 0
+    for low, high, zeros in ((-140, -132, False), (-126, -126, False), (-125, -112, True),
+                             (-112, -90, False), (-20, 10, True), (60, 90, False)):
+        announce(f"attn_q8 few rows, value scales 2^{low}..2^{high} {new} {lens} dim {dim} {dtype}")
+        _check_scaled(_scaled_cache(62, lens, 2, dim, 16, low, high, zeros), new, heads, dtype, q)
