@@ -304,7 +304,8 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
                                            !there[1] || !finite(vs[0] + vs[1]))) {
             // Some of the keys are hidden from some of the rows, or a page's
             // value scale is NaN: that goes into the scores, so that it stays
-            // with the rows that see it.
+            // with the rows that see it.  A page that a row does not see is
+            // not in its largest value scale either.
             const int lo = row.lo - t0 - 4 * g, hi = row.hi - t0 - 4 * g;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -313,7 +314,9 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
                     s[h][i] += finite(vs[h]) ? 0.0f : nan();
                     s[h][i] = there[h] && 16 * h + i >= lo && 16 * h + i < hi ? s[h][i] : neg_inf();
                 }
-                vs[h] = there[h] && finite(vs[h]) ? vs[h] : 0.0f;
+                const int k0 = t0 + 16 * h;
+                const bool sees = there[h] && row.lo < k0 + 16 && row.hi > k0;
+                vs[h] = sees && finite(vs[h]) ? vs[h] : 0.0f;
             }
         }
         float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
@@ -612,9 +615,10 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
         }
         return fmaxf(top[0] * by0, top[1] * by1);
     };
-    // The rows' references: the largest score and value scale so far, moved
-    // only when a key passes them by so much that p * vs would leave float16
-    // (2^15 at the reference, 2^0.99 above it still fits).
+    // The rows' references: the largest score and value scale of the keys that
+    // each has seen so far, moved only when a key passes them by so much that
+    // p * vs would leave float16 (2^15 at the reference, 2^0.99 above it still
+    // fits).
     auto refer = [&](float top, float lg_vs) {
         const float m_new = fmaxf(m, max_halves(top));
         const float lg_new = fmaxf(lg_run, lg_vs);
@@ -690,12 +694,12 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
 #pragma unroll
                 for (int h0 = 0; h0 < 2; h0 += HS) {
                     f16v s[HS];
-                    float by[2 * HS], top = neg_inf(), lg = neg_inf();
+                    float by[2 * HS], lg_vs[2 * HS], top = neg_inf(), lg = neg_inf();
                     scores(s, kp + 32 * h0 * KLD);
 #pragma unroll
-                    for (int h = 0; h < HS; ++h) {
-                        by[2 * h] = gp[2 * (h0 + h)].ks * to_log2;
-                        by[2 * h + 1] = gp[2 * (h0 + h) + 1].ks * to_log2;
+                    for (int u = 0; u < 2 * HS; ++u) {
+                        by[u] = gp[2 * h0 + u].ks * to_log2;
+                        lg_vs[u] = gp[2 * h0 + u].lg_vs;
                     }
                     if (h0 == 0) {
                         stage(buf ^ 1);
@@ -704,7 +708,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
                     if (!seen) {
                         // What is hidden from a row goes into its scores, and
                         // a value scale that is not finite too: so it stays
-                        // with the rows that see it.
+                        // with the rows that see it.  Scales of keys that a
+                        // row does not see are not in its reference.
 #pragma unroll
                         for (int h = 0; h < HS; ++h) {
                             const int t = t0 + 32 * (h0 + h) + 4 * g;
@@ -716,13 +721,18 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
                                 const float x = on & 2 ? nan() : s[h][j] * by[2 * h + j / 8];
                                 s[h][j] = on & 1 && at >= lo && at < hi ? x : neg_inf();
                             }
-                            by[2 * h] = by[2 * h + 1] = 1.0f;
+#pragma unroll
+                            for (int u = 2 * h; u < 2 * h + 2; ++u) {
+                                const int k0 = t0 + 32 * h0 + 16 * u;
+                                by[u] = 1.0f;
+                                lg_vs[u] = row.lo < k0 + 16 && row.hi > k0 ? lg_vs[u] : neg_inf();
+                            }
                         }
                     }
 #pragma unroll
                     for (int h = 0; h < HS; ++h) {
                         top = fmaxf(top, largest(s[h], by[2 * h], by[2 * h + 1]));
-                        lg = fmaxf(lg, fmaxf(gp[2 * (h0 + h)].lg_vs, gp[2 * (h0 + h) + 1].lg_vs));
+                        lg = fmaxf(lg, fmaxf(lg_vs[2 * h], lg_vs[2 * h + 1]));
                     }
                     refer(top, lg);
 #pragma unroll

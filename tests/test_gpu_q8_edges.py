@@ -253,3 +253,33 @@ def test_few_rows_over_small_and_distant_value_scales(new, lens, heads, dim, dty
                              (-112, -90, False), (-20, 10, True), (60, 90, False)):
         announce(f"attn_q8 few rows, value scales 2^{low}..2^{high} {new} {lens} dim {dim} {dtype}")
         _check_scaled(_scaled_cache(62, lens, 2, dim, 16, low, high, zeros), new, heads, dtype, q)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,lens,window,growth", [
+    ([2], [17], 0, 50), ([4], [28], 10, -50), ([3, 1, 2], [34, 20, 16], 0, 40),  # few rows
+    ([70], [70], 0, 25), ([70], [70], 20, -25), ([100], [700], 30, 3), ([100], [700], 30, -3),
+    ([260], [700], 40, -4)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scales_of_pages_that_only_other_rows_see(new, lens, window, growth, dim, dtype):
+    """Value scales that grow or fall from page to page by a power of two:
+    every row keeps its bits relative to the pages that it sees itself."""
+    announce(f"attn_q8 others' pages {new} {lens} window {window} 2^{growth} a page dim {dim} {dtype}")
+    c = Cache(63, lens, 1, dim, 16)
+    c.poison_unused()
+    for b, t in enumerate(lens):
+        cols = np.arange(-(-t // 16))
+        steps = cols if growth > 0 else cols[-1] - cols
+        c.vs[c.table[b, cols], 0] = np.exp2(abs(growth) * steps - 60.0).astype(np.float32)
+    rng = np.random.default_rng(4)
+    q = rng.normal(size=(sum(new), 2, dim))
+    out, lse, ref, rlse, tol = _attend(c, new, q, dtype, window=window)
+    # float16's smallest step: 2^-40 of the largest value scale that the row sees
+    cu = _cu(new)
+    for b, t in enumerate(lens):
+        for i in range(new[b]):
+            pos = t - new[b] + i
+            seen = np.arange((max(0, pos - window + 1) if window else 0) // 16, pos // 16 + 1)
+            tol[cu[b] + i] += 2.0 ** -40 * 127 * t * c.vs[c.table[b, seen], 0].max()
+    assert np.all(np.abs(out - ref) <= tol), (np.abs(out - ref) / tol).max()
+    assert np.all(np.abs(lse - rlse) <= 1e-3)
