@@ -16,6 +16,8 @@
 // two memory latencies and the reduction; the read-back of [8192, 8192]
 // 33 us (6.2 TB/s), of float32 rows of odd length 3.7 TB/s (their stores
 // straddle cache lines).
+#include <algorithm>
+
 #include "avae.h"
 #include "avae_internal.h"
 #include "q8.h"
@@ -290,17 +292,49 @@ hipError_t dequant_q8(const int8_t* q, long long ldq, const float* scale, int M,
 
 }  // namespace
 
+namespace {
+
+// A launch has fewer than 2^32 threads: rows go out in runs of this many.
+constexpr int kRun = 1 << 21;
+
+template <typename T>
+hipError_t rows_runs(const T* x, long long ldx, const T* res, long long ldr, const float* w, int M,
+                     int C, float eps, T* sum, long long lds, int8_t* q, long long ldq,
+                     float* scale, hipStream_t stream) {
+    hipError_t e = hipSuccess;
+    for (long long m = 0; m < M && e == hipSuccess; m += kRun)
+        e = rows_q8<T>(x + m * ldx, ldx, res ? res + m * ldr : nullptr, ldr, w,
+                       (int)std::min<long long>(M - m, kRun), C, eps,
+                       sum ? sum + m * lds : nullptr, lds, q + m * ldq, ldq, scale + m, stream);
+    return e;
+}
+
+template <typename T>
+hipError_t dequant_runs(const int8_t* q, long long ldq, const float* scale, int M, int C, T* y,
+                        long long ldy, hipStream_t stream) {
+    hipError_t e = hipSuccess;
+    for (long long m = 0; m < M && e == hipSuccess; m += kRun)
+        e = dequant_q8<T>(q + m * ldq, ldq, scale + m, (int)std::min<long long>(M - m, kRun), C,
+                          y + m * ldy, ldy, stream);
+    return e;
+}
+
+}  // namespace
+
 hipError_t launch_rows_q8(int dtype, const void* x, long long ldx, const void* res, long long ldr,
                           const float* w, int M, int C, float eps, void* sum, long long lds,
                           int8_t* q, long long ldq, float* scale, hipStream_t stream) {
     prof_pre(stream);
     hipError_t e;
     if (dtype == AVAE_F32)
-        e = rows_q8<float>(x, ldx, res, ldr, w, M, C, eps, sum, lds, q, ldq, scale, stream);
+        e = rows_runs((const float*)x, ldx, (const float*)res, ldr, w, M, C, eps, (float*)sum,
+                      lds, q, ldq, scale, stream);
     else if (dtype == AVAE_BF16)
-        e = rows_q8<__bf16>(x, ldx, res, ldr, w, M, C, eps, sum, lds, q, ldq, scale, stream);
+        e = rows_runs((const __bf16*)x, ldx, (const __bf16*)res, ldr, w, M, C, eps, (__bf16*)sum,
+                      lds, q, ldq, scale, stream);
     else
-        e = rows_q8<_Float16>(x, ldx, res, ldr, w, M, C, eps, sum, lds, q, ldq, scale, stream);
+        e = rows_runs((const _Float16*)x, ldx, (const _Float16*)res, ldr, w, M, C, eps, (_Float16*)sum,
+                      lds, q, ldq, scale, stream);
     const double n = (double)M * C, es = dtype == AVAE_F32 ? 4 : 2;
     prof_post(stream, "rows_q8_kernel", 6.0 * n, n * (es * (res ? 3 : 1) + 1));
     return e;
@@ -310,9 +344,9 @@ hipError_t launch_dequant_q8(int dtype, const int8_t* q, long long ldq, const fl
                              int C, void* y, long long ldy, hipStream_t stream) {
     prof_pre(stream);
     const hipError_t e =
-        dtype == AVAE_F32    ? dequant_q8<float>(q, ldq, scale, M, C, y, ldy, stream)
-        : dtype == AVAE_BF16 ? dequant_q8<__bf16>(q, ldq, scale, M, C, y, ldy, stream)
-                             : dequant_q8<_Float16>(q, ldq, scale, M, C, y, ldy, stream);
+        dtype == AVAE_F32    ? dequant_runs(q, ldq, scale, M, C, (float*)y, ldy, stream)
+        : dtype == AVAE_BF16 ? dequant_runs(q, ldq, scale, M, C, (__bf16*)y, ldy, stream)
+                             : dequant_runs(q, ldq, scale, M, C, (_Float16*)y, ldy, stream);
     const double n = (double)M * C;
     prof_post(stream, "dequant_q8_kernel", n, n * (1 + (dtype == AVAE_F32 ? 4 : 2)));
     return e;

@@ -283,3 +283,27 @@ def test_scales_of_pages_that_only_other_rows_see(new, lens, window, growth, dim
             tol[cu[b] + i] += 2.0 ** -40 * 127 * t * c.vs[c.table[b, seen], 0].max()
     assert np.all(np.abs(out - ref) <= tol), (np.abs(out - ref) / tol).max()
     assert np.all(np.abs(lse - rlse) <= 1e-3)
+
+
+def test_rows_past_one_launch():
+    """2^26 rows and a few: more than one launch has threads for."""
+    from bigvgan_waveform_decoder_amd import avae
+    announce("quant_q8, rms_norm_q8, dequant_q8 of 2^26 + 9 rows")
+    torch = _t()
+    M, C = (1 << 26) + 9, 16
+    x = torch.zeros((M, C), dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, (1 << 21) - 1, 1 << 21, (1 << 24) + 3, 1 << 26, M - 2, M - 1], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x[at] = torch.randn((len(at), C), device="cuda", generator=g).bfloat16()
+    w = torch.rand(C, device="cuda", generator=g)
+    for call in (avae.quant_q8, lambda t: avae.rms_norm_q8(t, w, residual=t)):
+        got, want = call(x), call(x[at])
+        for a, b in zip(got, want):
+            if b is not None:
+                assert torch.equal(a[at], b)
+        q, s = got[:2]
+        assert int((s != 0).sum()) == len(at) and int((q != 0).sum()) == int((q[at] != 0).sum())
+        y = avae.dequant_q8(q, s, dtype=torch.bfloat16)
+        assert torch.equal(y[at], avae.dequant_q8(q[at], s[at], dtype=torch.bfloat16))
+        assert int((y != 0).sum()) == int((y[at] != 0).sum())
+        del got, q, s, y
