@@ -208,8 +208,8 @@ extern "C" int avae_linear_q8(const signed char* a, long long lda, const float* 
     AVAE_CHECK(check_rows(who, "a", M, K, lda));
     AVAE_CHECK(check_rows(who, "w", N, K, ldw));
     AVAE_CHECK(check_rows(who, "y", M, N, ldy));
-    if (M > (1 << 21) || N > (1 << 28))
-        return abi_fail(AVAE_ESHAPE, "%s: M is over 2^21 or N over 2^28", who);
+    if (M > (1 << 21) || N >= (1 << 28))
+        return abi_fail(AVAE_ESHAPE, "%s: M is over 2^21 or N not under 2^28", who);
     const size_t need = avae::linear_q8_workspace_bytes(M, N, K);
     if (need && (!workspace || ws_bytes < need || misaligned(workspace, 16)))
         return abi_fail(AVAE_EWORKSPACE, "%s: %zu bytes of workspace, aligned to 16, are needed",

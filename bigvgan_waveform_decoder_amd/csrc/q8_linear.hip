@@ -430,12 +430,13 @@ __global__ __launch_bounds__(WGM* WGN * 64) void linear_q8_tile_kernel(LinearQ8 
 // row, the activations' first.
 __global__ __launch_bounds__(256) void pack_q8_kernel(LinearQ8 p, int8_t* __restrict__ out,
                                                       int width) {
-    const long long row = blockIdx.x * 4LL + (threadIdx.x >> 6);
-    if (row >= (long long)p.M + p.N) return;
-    const int8_t* from = row < p.M ? p.a + row * p.lda : p.w + (row - p.M) * p.ldw;
-    for (int k = (threadIdx.x & 63) * 16; k < width; k += 1024)
-        *reinterpret_cast<v4i*>(out + row * width + k) =
-            k + 16 <= p.K ? load16<false>(from, k) : load16_tail(from, k, p.K);
+    for (long long row = blockIdx.x * 4LL + (threadIdx.x >> 6); row < (long long)p.M + p.N;
+         row += gridDim.x * 4LL) {
+        const int8_t* from = row < p.M ? p.a + row * p.lda : p.w + (row - p.M) * p.ldw;
+        for (int k = (threadIdx.x & 63) * 16; k < width; k += 1024)
+            *reinterpret_cast<v4i*>(out + row * width + k) =
+                k + 16 <= p.K ? load16<false>(from, k) : load16_tail(from, k, p.K);
+    }
 }
 
 constexpr int kCus = 256;
@@ -515,8 +516,9 @@ hipError_t linear_q8(LinearQ8 p, void* ws, hipStream_t stream) {
     // first tiles on ([6000, 6143, 1535]: 104 us, 285 straight from memory)
     int8_t* rows = (int8_t*)ws;
     const int width = (p.K + 127) / 128 * 128;
-    hipLaunchKernelGGL(pack_q8_kernel, dim3((unsigned)(((long long)p.M + p.N + 3) / 4)), dim3(256),
-                       0, stream, p, rows, width);
+    // (a launch has fewer than 2^32 threads)
+    const unsigned groups = (unsigned)std::min(((long long)p.M + p.N + 3) / 4, 1LL << 22);
+    hipLaunchKernelGGL(pack_q8_kernel, dim3(groups), dim3(256), 0, stream, p, rows, width);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     p.a = rows;

@@ -552,7 +552,8 @@ int avae_dequant_q8(const signed char* q, long long ldq, const float* scale, int
  *   bases and strides that are multiples of 16 bytes are fastest.
  *   workspace: device, avae_linear_q8_workspace_bytes(M, N, K) (which may
  *   be 0) bytes, aligned to 16; its contents do not matter.
- * Errors: EINVAL, ESHAPE (K or a stride out of range), EWORKSPACE.
+ * Errors: EINVAL, ESHAPE (K or a stride out of range, M over 2^21, N not
+ *   under 2^28), EWORKSPACE.
  */
 #define AVAE_LINEAR_Q8_MAX_K 131071
 size_t avae_linear_q8_workspace_bytes(int M, int N, int K);

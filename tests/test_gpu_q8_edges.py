@@ -307,3 +307,20 @@ def test_rows_past_one_launch():
         assert torch.equal(y[at], avae.dequant_q8(q[at], s[at], dtype=torch.bfloat16))
         assert int((y != 0).sum()) == int((y[at] != 0).sum())
         del got, q, s, y
+
+
+def test_linear_of_more_columns_than_a_launch_packs():
+    """2^26 weight rows of odd length, laid out anew in one call."""
+    from bigvgan_waveform_decoder_amd import avae
+    announce("linear_q8 17 x 2^26 x 17")
+    torch = _t()
+    M, N, K = 17, (1 << 26) + 5, 17
+    assert avae.lib().avae_linear_q8_workspace_bytes(M, N, K) > 0
+    g = torch.Generator(device="cuda").manual_seed(5)
+    a = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    one = torch.ones(M, device="cuda")
+    y = avae.linear_q8(a, one, w, torch.ones(N, device="cuda"), dtype=torch.bfloat16)
+    at = torch.cat([torch.arange(64), torch.arange(N - 200, N), torch.randint(0, N, (2000,))]).cuda()
+    want = (a.cpu().double() @ w[at].cpu().double().t()).bfloat16()
+    assert torch.equal(y[:, at].cpu(), want)

@@ -172,3 +172,7 @@ def test_binding_checks_tensors():
     with pytest.raises(ValueError, match="device tensor"):
         avae.KvCacheQ8(*(torch.zeros((1, 1, 16, 64), dtype=torch.int8) for _ in range(2)),
                        *(torch.zeros((1, 1)) for _ in range(2)))
+
+
+def test_linear_columns_of_one_launch():
+    assert _linear(N=1 << 28, ldy=1 << 28) == ESHAPE
