@@ -16,6 +16,7 @@ using avae::Ragged;
 namespace {
 
 constexpr long long kMaxElems = 1LL << 46;  // keeps every byte offset in 64 bits
+constexpr long long kMaxGroups = (1 << 24) - 1;  // of 256 threads: under 2^32 a launch
 
 bool bad_dtype(int d) { return d != AVAE_F32 && d != AVAE_BF16 && d != AVAE_F16; }
 int elem_size(int d) { return d == AVAE_F32 ? 4 : 2; }
@@ -235,6 +236,9 @@ extern "C" int avae_kv_write_q8(const void* k, long long k_tok, long long k_head
     AVAE_CHECK(check_dtype(who, dtype, v, "v"));
     AVAE_CHECK(check_strides(who, "k", k_tok, k_head, r.total, c.heads, c.dim));
     AVAE_CHECK(check_strides(who, "v", v_tok, v_head, r.total, c.heads, c.dim));
+    if (avae::kv_write_q8_pages(c, r) > kMaxGroups)
+        return abi_fail(AVAE_ESHAPE, "%s: %d rows of one sequence at once touch more than 2^24 pages",
+                        who, r.max_rows);
     return done(avae::launch_kv_write_q8(dtype, k, k_tok, k_head, v, v_tok, v_head, c, r,
                                          (hipStream_t)stream),
                 who);
@@ -307,6 +311,13 @@ extern "C" int avae_attn_q8(const void* q, long long q_tok, long long q_head, in
     if (need && (!workspace || ws_bytes < need || misaligned(workspace, 16)))
         return abi_fail(AVAE_EWORKSPACE, "%s: %zu bytes of workspace, aligned to 16, are needed",
                         who, need);
+    const long long groups = avae::attn_q8_workgroups(
+        r.seqs, r.total, r.max_rows, max_len, q_heads, c.heads, c.dim, elem_size(dtype), window);
+    if (groups > kMaxGroups)
+        return abi_fail(AVAE_ESHAPE,
+                        "%s: %d sequences of up to %d rows are %lld workgroups, over 2^24: give the "
+                        "most rows that one has, or split the call",
+                        who, r.seqs, r.max_rows, groups);
     avae::AttnQ8 a{};
     a.q = q;
     a.q_tok = q_tok;

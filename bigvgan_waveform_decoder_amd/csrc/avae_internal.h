@@ -171,6 +171,9 @@ hipError_t launch_linear_q8(const int8_t* a, long long lda, const float* sa, con
                             long long ldw, const float* sw, const float* bias, int M, int N, int K,
                             int act, int dtype, void* y, long long ldy, void* ws,
                             hipStream_t stream);
+// Pages of a sequence that a write's launch covers: what max_rows tokens can
+// touch, at any place in the first of them, and no more than the table has.
+int kv_write_q8_pages(const CacheQ8& c, const Ragged& r);
 hipError_t launch_kv_write_q8(int dtype, const void* k, long long k_tok, long long k_head,
                               const void* v, long long v_tok, long long v_head, const CacheQ8& c,
                               const Ragged& r, hipStream_t stream);
@@ -188,6 +191,9 @@ struct AttnQ8 {
 };
 size_t attn_q8_workspace_bytes(int seqs, int total, int max_rows, int max_len, int q_heads,
                                int heads, int dim, int elem, int window);
+// Workgroups of 256 threads that the largest of its launches has.
+long long attn_q8_workgroups(int seqs, int total, int max_rows, int max_len, int q_heads,
+                             int heads, int dim, int elem, int window);
 hipError_t launch_attn_q8(int dtype, const AttnQ8& a, const CacheQ8& c, const Ragged& r, void* ws,
                           hipStream_t stream);
 

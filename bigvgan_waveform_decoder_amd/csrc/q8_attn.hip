@@ -940,12 +940,15 @@ Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int dim, in
     return r;
 }
 
+// Which join: a wave a row wants rows for the CUs ([1 x 2400 keys, 12 heads]
+// takes 15.6 us with it, 13.5 with a workgroup a row).
+bool join_by_waves(int splits, long long rows) { return splits <= 64 && rows >= 2048; }
+
 template <typename T, int D>
 hipError_t run(const AttnQ8& a, const CacheQ8& c, const Ragged& r, float* part,
                hipStream_t stream) {
     const Cut k = cut(r.seqs, r.max_rows, a.max_len, a.q_heads, c.heads, D, sizeof(T), a.window);
     const long long blocks = (long long)k.tiles * k.splits * c.heads * r.seqs;
-    if (blocks > 0xffffff) return hipErrorInvalidValue;  // 2^32 threads
     if (k.many)
         hipLaunchKernelGGL((attn_q8_many_kernel<T, D>),
                            dim3((unsigned)blocks),
@@ -958,9 +961,7 @@ hipError_t run(const AttnQ8& a, const CacheQ8& c, const Ragged& r, float* part,
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && k.splits > 1) {
         const int rows = r.total * a.q_heads;
-        // (a wave a row wants rows for the CUs: [1 x 2400 keys, 12 heads]
-        // takes 15.6 us with it, 13.5 with a workgroup a row)
-        if (k.splits <= 64 && rows >= 2048)
+        if (join_by_waves(k.splits, rows))
             hipLaunchKernelGGL((attn_q8_join_few_kernel<T, D>), dim3((unsigned)(rows + 3LL) / 4),
                                dim3(256), 0, stream, a, rows, k.splits, part);
         else
@@ -985,6 +986,15 @@ size_t attn_q8_workspace_bytes(int seqs, int total, int max_rows, int max_len, i
                                int heads, int dim, int elem, int window) {
     const Cut k = cut(seqs, max_rows, max_len, q_heads, heads, dim, elem, window);
     return k.splits > 1 ? (size_t)total * q_heads * k.splits * (dim + 4) * sizeof(float) : 0;
+}
+
+long long attn_q8_workgroups(int seqs, int total, int max_rows, int max_len, int q_heads,
+                             int heads, int dim, int elem, int window) {
+    const Cut k = cut(seqs, max_rows, max_len, q_heads, heads, dim, elem, window);
+    const long long blocks = (long long)k.tiles * k.splits * heads * seqs;
+    const long long rows = (long long)total * q_heads;
+    if (k.splits == 1) return blocks;
+    return std::max(blocks, join_by_waves(k.splits, rows) ? rows / 4 + 1 : 2 * rows);
 }
 
 hipError_t launch_attn_q8(int dtype, const AttnQ8& a, const CacheQ8& c, const Ragged& r, void* ws,

@@ -587,7 +587,8 @@ typedef struct avae_kv_q8 {
  *     tokens j*page .. (j+1)*page - 1 of the sequence.  Entries past a
  *     sequence's length are not read.
  *   total: rows of the packed tensors; max_rows: at least the most rows of
- *     one sequence (rows past it are not computed).
+ *     one sequence (rows past it are not computed).  Launches and the choice
+ *     of kernels go by it: give the true number where it is known.
  * The kernels check what the host cannot see: rows outside 0 .. total, a
  * table column past table_cols or an entry that is no page leave that token
  * out (not written; zeros when read; not seen by the attention).
@@ -644,8 +645,8 @@ int avae_kv_read_q8(const avae_kv_q8* cache, const avae_ragged* rows, int dtype,
  * float32 queries are multiplied with 22 of their 24 bits, and so are the
  * probabilities for float32 output (11 for 16-bit outputs), down to 2^-40 of
  * the row's largest probability and value scale; the sums are float32.
- * Errors: EINVAL, ESHAPE (head counts, dim, page, max_len over the table),
- *   EWORKSPACE.
+ * Errors: EINVAL, ESHAPE (head counts, dim, page, max_len over the table,
+ *   more sequences times max_rows than one launch takes), EWORKSPACE.
  */
 size_t avae_attn_q8_workspace_bytes(const avae_kv_q8* cache, const avae_ragged* rows, int q_heads,
                                     int dtype, int max_len, int window);

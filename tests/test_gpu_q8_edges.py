@@ -324,3 +324,32 @@ def test_linear_of_more_columns_than_a_launch_packs():
     at = torch.cat([torch.arange(64), torch.arange(N - 200, N), torch.randint(0, N, (2000,))]).cuda()
     want = (a.cpu().double() @ w[at].cpu().double().t()).bfloat16()
     assert torch.equal(y[:, at].cpu(), want)
+
+
+def test_bounds_on_rows_far_past_them():
+    """max_rows and total of 2^28 where a sequence has a few rows: the write and
+    the read of the cache go by what there is."""
+    import ctypes
+    from bigvgan_waveform_decoder_amd import avae
+    announce("kv_write_q8, kv_read_q8 with bounds of 2^28 rows")
+    torch = _t()
+    new, lens = [20, 3], [50, 3]
+    c = Cache(54, lens, 2, 64, 16)
+    dev, cu = c.upload(), _cu([20, 3])
+    table, dcu, dlens = _dev(c.table), _dev(cu), _dev(c.lens)
+    rng = np.random.default_rng(1)
+    x = rng.normal(size=(23, 2, 64)).astype(np.float32)
+    dx = _dev(x)
+    rows = avae.avae_ragged(dcu.data_ptr(), dlens.data_ptr(), table.data_ptr(), c.table.shape[1],
+                            c.table.shape[1], 2, 1 << 28, 1 << 28)
+    stream = torch.cuda.current_stream().cuda_stream
+    L = avae.lib()
+    assert L.avae_kv_write_q8(dx.data_ptr(), 128, 64, dx.data_ptr(), 128, 64, 0, dev.ref,
+                              ctypes.byref(rows), stream) == 0
+    for q8, s in ((c.k8, c.ks), (c.v8, c.vs)):
+        R.kv_write(q8, s, x, c.table, cu, lens, c.n, 16)
+    assert c.same()
+    k, v = (torch.full((23, 2, 64), 7.0, device="cuda") for _ in range(2))
+    assert L.avae_kv_read_q8(dev.ref, ctypes.byref(rows), 0, k.data_ptr(), v.data_ptr(), stream) == 0
+    assert np.array_equal(_np(k), R.kv_read(c.k8, c.ks, c.table, cu, lens, 16))
+    assert np.array_equal(_np(v), R.kv_read(c.v8, c.vs, c.table, cu, lens, 16))

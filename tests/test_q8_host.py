@@ -176,3 +176,18 @@ def test_binding_checks_tensors():
 
 def test_linear_columns_of_one_launch():
     assert _linear(N=1 << 28, ldy=1 << 28) == ESHAPE
+
+
+def test_more_work_than_a_launch_takes():
+    """Bounds of the rows that are far from the truth are refused by name."""
+    L = avae.lib()
+    many = dict(seqs=60000, total=1 << 20, max_rows=1 << 20)
+    assert _attn(rows=_rows(**many)) == ESHAPE
+    assert b"workgroups" in L.avae_last_error() and b"split the call" in L.avae_last_error()
+    # (few rows over split keys, in packed rows far longer than they are)
+    assert _attn(cache=_cache(n_pages=1000), max_len=40000, ws_bytes=1 << 62,
+                 rows=_rows(table_cols=2500, table_ld=2500, seqs=1, total=1 << 25, max_rows=1)) == ESHAPE
+    assert b"workgroups" in L.avae_last_error()
+    c, r = _cache(), _rows(table_cols=1 << 25, table_ld=1 << 25, total=1 << 30, max_rows=1 << 29)
+    assert L.avae_kv_write_q8(A, 128, 64, B, 128, 64, 1, ctypes.byref(c), ctypes.byref(r), None) == ESHAPE
+    assert b"2^24 pages" in L.avae_last_error()
