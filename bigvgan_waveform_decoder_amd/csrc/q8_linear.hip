@@ -73,11 +73,15 @@ __device__ inline v4i load16_tail(const int8_t* row, int k, int K) {
     return v;
 }
 
-template <bool SILU>
+// SiLU's quick exponential is off by |v| 2^-23 of itself at most, under 2^-16
+// where it is not 0: nothing to a 16-bit output.  A float32 one is computed to
+// its own rounding.
+template <typename T, bool SILU>
 __device__ inline float epilogue(int acc, float sa, float sw, float bias) {
-    float v = fmaf((float)acc * sa, sw, bias);
-    if (SILU) v *= __builtin_amdgcn_rcpf(1.0f + __expf(-v));
-    return v;
+    const float v = fmaf((float)acc * sa, sw, bias);
+    if (!SILU) return v;
+    if (sizeof(T) == 4) return v / (1.0f + expf(-v));
+    return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
 }
 
 // Four outputs of row m from column n on: their scales, and the store.
@@ -103,7 +107,7 @@ __device__ inline void store4(const LinearQ8& p, int m, int n, v4i acc, const Sc
     Pack<T, 4> out;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        out.v[r] = round_to<T>(epilogue<SILU>(acc[r], s.sa, s.sw[r], s.bias[r]));
+        out.v[r] = round_to<T>(epilogue<T, SILU>(acc[r], s.sa, s.sw[r], s.bias[r]));
     if (p.yvec) {
         *reinterpret_cast<Pack<T, 4>*>(y) = out;
     } else if (n + 4 <= p.N) {
@@ -404,7 +408,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void linear_q8_tile_kernel(LinearQ8 
                 Pack<T, E> out;
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    out.v[e] = round_to<T>(epilogue<SILU>(acc[(c + e) / 4][v][(c + e) % 4], sa[v],
+                    out.v[e] = round_to<T>(epilogue<T, SILU>(acc[(c + e) / 4][v][(c + e) % 4], sa[v],
                                                           sw[c + e], bias[c + e]));
                 if (p.yvec) {
                     // past the caches, which the operands need

@@ -353,3 +353,23 @@ def test_bounds_on_rows_far_past_them():
     assert L.avae_kv_read_q8(dev.ref, ctypes.byref(rows), 0, k.data_ptr(), v.data_ptr(), stream) == 0
     assert np.array_equal(_np(k), R.kv_read(c.k8, c.ks, c.table, cu, lens, 16))
     assert np.array_equal(_np(v), R.kv_read(c.v8, c.vs, c.table, cu, lens, 16))
+
+
+@pytest.mark.parametrize("M,N", [(3, 512), (600, 640), (1500, 2048)])
+def test_silu_in_float32_to_its_last_bits(M, N):
+    """Exact sums with power-of-two scales: what is left is SiLU's own error, an
+    exponential within one last place, an addition and a division.  Below -88 the
+    exponential is past float32 and the value, under 3e-37, is 0."""
+    from bigvgan_waveform_decoder_amd import avae
+    announce(f"linear_q8 SiLU float32 {M}x{N}")
+    torch = _t()
+    rng = np.random.default_rng(N)
+    a = rng.integers(-127, 128, size=(M, 64)).astype(np.int8)
+    w = rng.integers(-127, 128, size=(N, 64)).astype(np.int8)
+    a[0] = w[0]
+    sw = np.exp2(rng.integers(-14, -9, size=N)).astype(np.float32)
+    y = avae.linear_q8(_dev(a), torch.ones(M, device="cuda"), _dev(w), _dev(sw), act="silu")
+    raw = R.linear_q8(a, np.ones(M, np.float32), w, sw)
+    assert raw.min() < -80 and raw.max() > 80 and np.array_equal(raw, raw.astype(np.float32))
+    ref = R.linear_q8(a, np.ones(M, np.float32), w, sw, act="silu")
+    assert np.all(np.abs(_np(y) - ref) <= 6 * U * np.abs(ref) + 3e-37)
