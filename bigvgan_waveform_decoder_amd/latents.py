@@ -167,6 +167,8 @@ class LatentGenerator:
     def generate(self, prompts: Sequence[torch.Tensor], frames: int) -> torch.Tensor:
         """`frames` new frames of each stream after its prompt -> latent
         [streams, c_latent, frames], as the decoder takes it."""
+        if frames < 1:
+            raise ValueError(f"frames must be at least 1, got {frames}")
         out: List[torch.Tensor] = [self.prefill(prompts)]
         while len(out) < frames:
             out.append(self.step(out[-1]))

@@ -107,3 +107,16 @@ def test_generator_refusals():
         gen.prefill([one, one])
     with pytest.raises(ValueError, match="frames are written"):
         gen.step(one)
+
+
+def test_generate_refuses_no_frames():
+    """No frame asked for is an error, and leaves the generator empty."""
+    import torch
+    from bigvgan_waveform_decoder_amd.latents import LatentGenerator, random_weights
+    cfg = _config()
+    gen = LatentGenerator(cfg, random_weights(cfg), 1, 20)
+    one = torch.zeros((1, cfg.c_latent), device="cuda")
+    for frames in (0, -3):
+        with pytest.raises(ValueError, match="frames must be at least 1"):
+            gen.generate([one], frames)
+    assert gen.generate([one], 1).shape == (1, cfg.c_latent, 1)
