@@ -81,7 +81,8 @@ __device__ inline float epilogue(int acc, float sa, float sw, float bias) {
     const float v = fmaf((float)acc * sa, sw, bias);
     if (!SILU) return v;
     if (sizeof(T) == 4) return v / (1.0f + expf(-v));
-    return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+    // (in eighths: the reciprocal of a number over 2^126 would be 0)
+    return 0.125f * v * __builtin_amdgcn_rcpf(fmaf(0.125f, __expf(-v), 0.125f));
 }
 
 // Four outputs of row m from column n on: their scales, and the store.

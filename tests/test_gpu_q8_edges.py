@@ -373,3 +373,21 @@ def test_silu_in_float32_to_its_last_bits(M, N):
     assert raw.min() < -80 and raw.max() > 80 and np.array_equal(raw, raw.astype(np.float32))
     ref = R.linear_q8(a, np.ones(M, np.float32), w, sw, act="silu")
     assert np.all(np.abs(_np(y) - ref) <= 6 * U * np.abs(ref) + 3e-37)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_silu_to_where_its_exponential_ends(dtype):
+    """From -89 to -80: bfloat16 outputs end where float32's do."""
+    from bigvgan_waveform_decoder_amd import avae
+    announce(f"linear_q8 SiLU around -88 {dtype}")
+    torch = _t()
+    a = torch.ones((1, 64), dtype=torch.int8, device="cuda")
+    w = torch.zeros((577, 64), dtype=torch.int8, device="cuda")
+    v = torch.arange(577, device="cuda") / 64 - 89.0  # exact: -80 and a bias
+    w[:, 0] = -80
+    y = avae.linear_q8(a, torch.ones(1, device="cuda"), w, torch.ones(577, device="cuda"), bias=v + 80,
+                       act="silu", dtype=_dtype(dtype))[0].double()
+    v = v.double()
+    ref = v / (1 + torch.exp(-v))
+    rel, _ = ROUND[dtype]
+    assert bool(((y - ref).abs() <= (rel + (6 * U if dtype == "f32" else 2.0 ** -16)) * ref.abs() + 3e-37).all())
