@@ -391,3 +391,40 @@ def test_silu_to_where_its_exponential_ends(dtype):
     ref = v / (1 + torch.exp(-v))
     rel, _ = ROUND[dtype]
     assert bool(((y - ref).abs() <= (rel + (6 * U if dtype == "f32" else 2.0 ** -16)) * ref.abs() + 3e-37).all())
+
+
+# M, N, K, first column and columns left over of wider tensors: a tile kernel each
+TILES = [(512, 1541, 400, 0, 0), (512, 1536, 256, 0, 0), (700, 1100, 112, 16, 32),  # 64 x 64
+         (2000, 2500, 1552, 0, 0), (1500, 4100, 64, 0, 16),                         # 64 x 128
+         (6000, 6144, 1536, 0, 0), (5900, 6200, 688, 0, 0),                         # 192 x 256, in rounds
+         (4096, 4096, 320, 0, 0), (8000, 8100, 272, 0, 0),                          # 256 x 256, in rounds
+         (600, 1541, 416, 3, 2), (2000, 2500, 208, 0, 1), (520, 1600, 48, 1, 0),    # through registers
+         (1000, 1000, 77, 0, 0), (2100, 2300, 1001, 5, 2), (4096, 4096, 300, 0, 0)]  # laid out anew
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,N,K,at,pad", TILES)
+def test_linear_tiles(M, N, K, at, pad, dtype):
+    """Sums that float32 holds: plain outputs have to be equal, SiLU's within
+    its own error (an exponential, an addition and a division; 2^-16 quick)."""
+    from bigvgan_waveform_decoder_amd import avae
+    announce(f"linear_q8 tiles {M}x{N}x{K} at {at} pad {pad} {dtype}")
+    torch = _t()
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    a, w = (torch.randint(-127, 128, (r, at + K + pad), dtype=torch.int8, device="cuda", generator=g)
+            for r in (M, N))
+    sa = torch.exp2(torch.randint(-4, 1, (M,), device="cuda", generator=g).float())
+    sw = torch.exp2(torch.randint(-11, -8, (N,), device="cuda", generator=g).float())
+    bias = torch.randint(-64, 65, (N,), device="cuda", generator=g) / 64.0
+    a, w = a[:, at:at + K], w[:, at:at + K]
+    raw = torch.mm(a.double(), w.t().double().contiguous()) * sa.double()[:, None] * sw.double()
+    y = avae.linear_q8(a, sa, w, sw, dtype=_dtype(dtype))
+    assert torch.equal(y, raw.to(_dtype(dtype)))
+    del y
+    y = avae.linear_q8(a, sa, w, sw, bias=bias, act="silu", dtype=_dtype(dtype)).double()
+    raw += bias.double()
+    assert torch.equal(raw, raw.float().double())
+    raw /= 1 + torch.exp(-raw)
+    rel, step = ROUND[dtype]
+    rel += 6 * U if dtype == "f32" else 2.0 ** -16
+    assert bool(((y - raw).abs() <= rel * raw.abs() + step + 3e-37).all())

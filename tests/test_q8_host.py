@@ -191,3 +191,23 @@ def test_more_work_than_a_launch_takes():
     c, r = _cache(), _rows(table_cols=1 << 25, table_ld=1 << 25, total=1 << 30, max_rows=1 << 29)
     assert L.avae_kv_write_q8(A, 128, 64, B, 128, 64, 1, ctypes.byref(c), ctypes.byref(r), None) == ESHAPE
     assert b"2^24 pages" in L.avae_last_error()
+
+
+@pytest.mark.parametrize("M,N,K", [(1000, 1000, 77), (64, 10000, 1001), (6000, 6143, 1535)])
+def test_linear_workspace_of_odd_rows(M, N, K):
+    """Products large enough for tiles with rows of odd length do need one."""
+    need = avae.lib().avae_linear_q8_workspace_bytes(M, N, K)
+    assert need >= (M + N) * K
+    kw = dict(M=M, N=N, K=K, lda=K, ldw=K, ldy=N)
+    for bad in (dict(ws_bytes=need - 1), dict(ws=None), dict(ws=ODD), dict(ws_bytes=0)):
+        assert _linear(**kw, **bad) == EWORKSPACE
+
+
+def test_attention_workspace_of_split_keys():
+    c = _cache(n_pages=1000)
+    rows = dict(table_cols=500, table_ld=500, seqs=1, total=1, max_rows=1)
+    need = avae.lib().avae_attn_q8_workspace_bytes(ctypes.byref(c), ctypes.byref(_rows(**rows)), 4, 1,
+                                                   8000, 0)
+    assert need > 0
+    for bad in (dict(ws_bytes=need - 1), dict(ws=None), dict(ws=ODD), dict(ws_bytes=0)):
+        assert _attn(cache=c, rows=_rows(**rows), max_len=8000, **bad) == EWORKSPACE
