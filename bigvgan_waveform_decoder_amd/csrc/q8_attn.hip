@@ -164,7 +164,7 @@ struct Query {
         }
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 120);
+        const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 127);
         const float up = __uint_as_float((unsigned)(127 + 14 - e) << 23);
         back = __uint_as_float((unsigned)(127 - 14 + e) << 23);
 #pragma unroll
@@ -501,7 +501,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf((float)q[16 * j + 8 * g + i]));
         top = max_halves(top);
-        const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 120);
+        const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 127);
         const float up = copysignf(__uint_as_float((unsigned)(127 + 14 - e) << 23), a.scale);
         to_log2 = __uint_as_float((unsigned)(127 - 14 + e) << 23) * fabsf(a.scale) * kLog2e;
 #pragma unroll

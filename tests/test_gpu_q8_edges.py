@@ -428,3 +428,23 @@ def test_linear_tiles(M, N, K, at, pad, dtype):
     rel, step = ROUND[dtype]
     rel += 6 * U if dtype == "f32" else 2.0 ** -16
     assert bool(((y - raw).abs() <= rel * raw.abs() + step + 3e-37).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,lens", [([2], [300]), ([90], [200])])
+@pytest.mark.parametrize("power", [-110, -60, 60, 119, 121, 124, 125])
+def test_queries_over_the_whole_range(power, new, lens, dtype):
+    """Queries times a power of two, the softmax's scale over it: the same
+    attention, up to float32's largest numbers."""
+    announce(f"attn_q8 queries times 2^{power} {new} {lens} {dtype}")
+    c = Cache(55, lens, 2, 64, 32)
+    c.poison_unused()
+    rng = np.random.default_rng(6)
+    q = np.clip(rng.normal(size=(sum(new), 4, 64)), -3.9, 3.9)
+    cu = _cu(new)
+    dq, qf = _typed(q * 2.0 ** power, dtype)
+    assert np.isfinite(qf).all()
+    out = _np(c.avae.attn_q8(dq, c.upload(), _dev(c.table), _dev(cu), _dev(c.lens),
+                             scale=0.125 * 2.0 ** -power))
+    want, _, _, _, tol = _attend(c, new, q, dtype)  # dim 64: its own scale is 0.125
+    assert np.all(np.abs(out - want) <= tol)
