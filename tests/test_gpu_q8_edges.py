@@ -448,3 +448,29 @@ def test_queries_over_the_whole_range(power, new, lens, dtype):
                              scale=0.125 * 2.0 ** -power))
     want, _, _, _, tol = _attend(c, new, q, dtype)  # dim 64: its own scale is 0.125
     assert np.all(np.abs(out - want) <= tol)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 64), (6, 2, 128), (2, 2, 256)])
+@pytest.mark.parametrize("window", [0, 700])
+def test_prompt_and_single_tokens_in_one_call(window, heads, kv_heads, dim, dtype):
+    """A prompt, drafts and single tokens over long keys, packed together; the
+    same call again gives the same bits."""
+    announce(f"attn_q8 mixed {heads}/{kv_heads} dim {dim} window {window} {dtype}")
+    new, lens = [1, 300, 1, 0, 1, 7], [3000, 340, 2500, 90, 1, 1900]
+    c = Cache(56, lens, kv_heads, dim, 64)
+    c.poison_unused()
+    rng = np.random.default_rng(7)
+    q = rng.normal(size=(sum(new), heads, dim)) * 2
+    first = np.array([5, 0, 2400, 0, 0, 100], np.int32)
+    for f in (None, first):
+        out, lse, ref, rlse, tol = _attend(c, new, q, dtype, window=window, first=f)
+        assert np.all(np.abs(out - ref) <= tol)
+        assert np.all(np.abs(lse - rlse) <= 1e-3)
+        again, lse2 = _attend(c, new, q, dtype, window=window, first=f)[:2]
+        assert np.array_equal(out, again) and np.array_equal(lse, lse2)
+    # the single tokens alone
+    for b, row in ((0, 0), (2, 301), (4, 302)):
+        one = [int(i == b) for i in range(len(new))]
+        out = _attend(c, one, q[row:row + 1], dtype, window=window, first=first)[0]
+        assert np.all(np.abs(out - ref[row:row + 1]) <= tol[row:row + 1])
