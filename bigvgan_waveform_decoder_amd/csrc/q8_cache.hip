@@ -112,38 +112,35 @@ __global__ __launch_bounds__(kThreads) void kv_write_q8_kernel(
 
 // A wave a token: 16 bytes of keys and of values a lane and step.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void kv_read_q8_kernel(CacheQ8 c, Ragged r,
+__global__ __launch_bounds__(kThreads) void kv_read_q8_kernel(CacheQ8 c, Ragged r, int from,
                                                               T* __restrict__ k,
                                                               T* __restrict__ v) {
     const int b = blockIdx.y, lane = threadIdx.x & 63;
     int cu0, n, len;
-    if (!ragged_rows(r, b, cu0, n, len)) return;
+    const int i = from + blockIdx.x * 4 + wave_id();  // the i-th of the sequence's last n tokens
+    if (!ragged_rows(r, b, cu0, n, len) || i >= n) return;
+    const int pos = len - n + i;
+    const int col = pos >> c.shift;
+    const int page = pos >= 0 ? page_of(c, b, col) : -1;
     const int row = c.heads * c.dim, dim_shift = __builtin_ctz(c.dim);
+    const long long out = (long long)(cu0 + i) * row;
     constexpr int N = 16 / sizeof(T);
-    // the i-th of the sequence's last n tokens
-    for (int i = blockIdx.x * 4 + wave_id(); i < n; i += 4 * gridDim.x) {
-        const int pos = len - n + i;
-        const int col = pos >> c.shift;
-        const int page = pos >= 0 ? page_of(c, b, col) : -1;
-        const long long out = (long long)(cu0 + i) * row;
-        for (int j = lane * N; j < row; j += 64 * N) {
-            float kv[N] = {}, vv[N] = {};
-            if (page >= 0) {
-                const long long at = (long long)page * c.heads + (j >> dim_shift);
-                const long long e =
-                    (at * c.page + (pos & (c.page - 1))) * c.dim + (j & (c.dim - 1));
-                load_stored<N>(c.k + e, N, kv);
-                load_stored<N>(c.v + e, N, vv);
-                const float ks = c.k_scale[at], vs = c.v_scale[at];
+    for (int j = lane * N; j < row; j += 64 * N) {
+        float kv[N] = {}, vv[N] = {};
+        if (page >= 0) {
+            const long long at = (long long)page * c.heads + (j >> dim_shift);
+            const long long e = (at * c.page + (pos & (c.page - 1))) * c.dim + (j & (c.dim - 1));
+            load_stored<N>(c.k + e, N, kv);
+            load_stored<N>(c.v + e, N, vv);
+            const float ks = c.k_scale[at], vs = c.v_scale[at];
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    kv[i] *= ks;
-                    vv[i] *= vs;
-                }
+            for (int i = 0; i < N; ++i) {
+                kv[i] *= ks;
+                vv[i] *= vs;
             }
-            stream_values(k + out + j, N, kv);
-            stream_values(v + out + j, N, vv);
         }
+        stream_values(k + out + j, N, kv);
+        stream_values(v + out + j, N, vv);
     }
 }
 
@@ -170,8 +167,12 @@ hipError_t kv_write(const void* k, long long k_tok, long long k_head, const void
 template <typename T>
 hipError_t kv_read(const CacheQ8& c, const Ragged& r, void* k, void* v, hipStream_t stream) {
     // (a launch has fewer than 2^32 threads a dimension)
-    const dim3 grid((unsigned)std::min((r.max_rows + 3LL) / 4, 1LL << 22), r.seqs);
-    hipLaunchKernelGGL(kv_read_q8_kernel<T>, grid, dim3(kThreads), 0, stream, c, r, (T*)k, (T*)v);
+    constexpr int kRun = 1 << 24;
+    for (long long from = 0; from < r.max_rows; from += kRun) {
+        const long long rows = std::min<long long>(r.max_rows - from, kRun);
+        hipLaunchKernelGGL(kv_read_q8_kernel<T>, dim3((unsigned)((rows + 3) / 4), r.seqs),
+                           dim3(kThreads), 0, stream, c, r, (int)from, (T*)k, (T*)v);
+    }
     return hipGetLastError();
 }
 
