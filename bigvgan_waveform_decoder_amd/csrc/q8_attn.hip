@@ -635,13 +635,12 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
     };
     // Probabilities of 16 keys times their value scale, in the accumulators'
     // units and straight from the exponent; the sum of the probabilities is
-    // theirs over the same factor.
+    // theirs over the same factor, kept 2^15 times as large: the factor alone
+    // would leave float32 for the smallest value scales.
     auto weigh = [&](const f16v& s, int u, float by, const Group& gr, h8& ph, h8& pl) {
         const float m_at = m == neg_inf() ? 0.0f : m;
         const float lift = fmaxf(gr.lg_vs + 15.0f - lg_run, -60.0f) - m_at;
-        // (in two halves: the units of small value scales are below float32)
-        const float half = __builtin_amdgcn_exp2f(0.5f * (lg_run - 15.0f));
-        const float drop = fminf(gr.vs * half * half, 0x1p60f);
+        const float drop = fminf(gr.vs * __builtin_amdgcn_exp2f(lg_run), 0x1p75f);
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -747,10 +746,11 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
         }
     }
 
-    l += __shfl_xor(l, 32);
+    l = (l + __shfl_xor(l, 32)) * 0x1p-15f;
     if (!row.live) return;
     const long long out_row = (long long)row.tok * a.q_heads + row.q_head;
-    const float half = __builtin_amdgcn_exp2f(0.5f * (lg_run - 15.0f));  // of the units, as above
+    // the unit in two halves, since it may be below float32
+    const float half = __builtin_amdgcn_exp2f(0.5f * (lg_run - 15.0f));
     const float by = splits > 1 ? half : l == 0.0f ? 0.0f : half / l;  // a NaN sum stays NaN
     float* pr = part + (out_row * splits + split) * (D + 4);
     // dims 4 p .. 4 p + 3 are in rows p, D / 4 + p, D / 2 + p, 3 D / 4 + p of
