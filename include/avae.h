@@ -643,8 +643,10 @@ int avae_kv_read_q8(const avae_kv_q8* cache, const avae_ragged* rows, int dtype,
  *   bytes, aligned to 16; its contents do not matter.  Of `rows` and
  *   `cache` the query reads only the sizes.
  * float32 queries are multiplied with 22 of their 24 bits, and so are the
- * probabilities for float32 output (11 for 16-bit outputs), down to 2^-40 of
- * the row's largest probability and value scale; the sums are float32.
+ * probabilities for float32 and float16 outputs (11 for bfloat16's), down to
+ * 2^-40 of the largest probability and value scale that the row sees; the sums
+ * are float32.  A row that sees a scale of NaN or infinity is NaN, in lse too.
+ * Value scales under 2^-126 may count as 0.
  * Errors: EINVAL, ESHAPE (head counts, dim, page, max_len over the table,
  *   more sequences times max_rows than one launch takes), EWORKSPACE.
  */

@@ -474,3 +474,19 @@ def test_prompt_and_single_tokens_in_one_call(window, heads, kv_heads, dim, dtyp
         one = [int(i == b) for i in range(len(new))]
         out = _attend(c, one, q[row:row + 1], dtype, window=window, first=first)[0]
         assert np.all(np.abs(out - ref[row:row + 1]) <= tol[row:row + 1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new,lens", [([1, 2], [700, 350]), ([1], [4000]), ([90], [600]), ([40], [1300])])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention_error_is_its_outputs_rounding(dim, new, lens, dtype):
+    """Root mean square over an output: a correctly rounded result's error, and a
+    tenth more for all that comes before the rounding."""
+    announce(f"attn_q8 error {new} {lens} dim {dim} {dtype}")
+    c = Cache(57, lens, 2, dim, 64)
+    c.poison_unused()
+    rng = np.random.default_rng(8)
+    q = rng.normal(size=(sum(new), 8, dim))
+    out, _, ref, _, _ = _attend(c, new, q, dtype)
+    best = _t().from_numpy(ref).to(_dtype(dtype)).double().numpy()
+    assert np.sqrt(np.mean((out - ref) ** 2)) <= 1.1 * np.sqrt(np.mean((best - ref) ** 2))
