@@ -1112,7 +1112,8 @@ def _heads(t, name: str, heads: Optional[int], dim: int):
 def kv_write_q8(cache: KvCacheQ8, k, v, table, cu, lens, max_new: Optional[int] = None,
                 stream=None):
     """avae_kv_write_q8: k, v [tokens, heads, dim] into the cache's pages.
-    max_new: at least the most rows of one sequence (all of them if not given)."""
+    max_new: at least the most rows of one sequence (all of them if not given;
+    the launch goes by it)."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return kv_write_q8(cache, k, v, table, cu, lens, max_new)
@@ -1153,8 +1154,10 @@ def attn_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = None,
             window: int = 0, first=None, return_lse: bool = False, stream=None):
     """avae_attn_q8: q [tokens, q_heads, dim] over the cache -> the same shape
     (and lse [tokens, q_heads] float32 if asked for).  max_q: at least the most
-    rows of one sequence; max_len: at least the longest sequence (the table's
-    tokens if not given); scale: 1 / sqrt(dim) if not given."""
+    rows of one sequence (all of them if not given, which is slow for many
+    short ones: the kernel is chosen by it); max_len: at least the longest
+    sequence (the table's tokens if not given); scale: 1 / sqrt(dim) if not
+    given."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return attn_q8(q, cache, table, cu, lens, max_q, max_len, scale, causal, window, first,

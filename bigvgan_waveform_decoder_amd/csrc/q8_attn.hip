@@ -455,10 +455,12 @@ struct alignas(16) Group {
 //
 // Bound by vector and matrix instructions in turn: of a step's cycles the
 // vector unit is busy 53% and the matrix cores 32%.  Measured, bfloat16:
-// 2 x 4096 rows on as many keys, 16 heads of 128, 400 us without order (687
-// TFLOP/s), 218-224 causal (620); float32 (split operands) 300; heads of 64
-// 144.  Two workgroups of four waves a CU: one of eight shares the staging
-// but keeps step, 521 against 427 us.
+// 2 x 4096 rows on as many keys, 16 heads of 128, 400-408 us without order
+// (675-687 TFLOP/s), 219-225 causal (620); float16 275-286, float32 303-312
+// (split operands); heads of 64 146; 8 heads of 256 304-319, float32 462: that
+// kernel alone spills, 26 registers a lane to 108 bytes of scratch.  Two
+// workgroups of four waves a CU: one of eight shares the staging but keeps
+// step, 521 against 427 us.
 template <typename T, int D>
 __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_kernel(AttnQ8 a, CacheQ8 c, Ragged r,
                                                            int splits, int chunk, int tiles,
@@ -919,6 +921,11 @@ Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int dim, in
     const int group = q_heads / heads;
     const long long rows = (long long)max_rows * group;
     Cut r;
+    // Either side of the limit, few / many rows' kernel in us, bfloat16, 12
+    // over 4 heads of 128: [1 x 2400 keys] 30 rows 15.6 / 16.9, 33 rows 15.8 /
+    // 17.1, 63 rows 20.6 / 18.4; [1 x 24000] 31 / 25, 30 / 25, 40 / 28; [64 x
+    // 4000] 100 / 102, 116 / 105, 136 / 107.  (float32 would stay with the
+    // first up to about 64 rows: [64 x 4000], 33 rows, 112 / 149.)
     r.many = rows > 32;
     const int height = r.many ? 32 * kWaves : 16, step = r.many ? 64 : 32 * kWaves;
     r.tiles = (int)((rows + height - 1) / height);

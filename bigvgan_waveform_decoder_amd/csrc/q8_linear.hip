@@ -17,7 +17,10 @@
 // 2048 of products a step); [6000, 6144, 1536] 80-83 us, whose twelve steps a
 // tile leave the outputs' writes and the SiLU of 96 values a thread a third
 // of the time; [37, 1536, 6144] 11.0 us and [1, 4608, 1536] 4.0 us (an empty
-// kernel takes 1.8): latency, with every load of a wave in flight at once.
+// kernel takes 1.8): latency.  A wave goes through its steps in batches and a
+// remainder of single ones, which wait for their loads one after the other
+// (all four of a wave's steps at K = 1536 with up to 32 rows), and as built a
+// batch has up to seven loads in flight, not all of its 24.
 #include <algorithm>
 
 #include "avae.h"
@@ -150,7 +153,8 @@ __global__ __launch_bounds__(512) void linear_q8_rows_kernel(LinearQ8 p) {
     const int s1 = min((wave + 1) * per, steps), full = min(s1, p.K / 64);
     int s = wave * per;
     v4i acc[NT][MT] = {};
-    // steps whose operands are in flight together: as many as 96 registers hold
+    // steps of a batch: as many as 96 registers hold the operands of (the
+    // compiler spreads their loads among the products)
     constexpr int U = 24 / (MT + NT) < 8 ? 24 / (MT + NT) : 8;
     for (; s + U <= full; s += U) {
         v4i wv[U][NT], av[U][MT];
@@ -484,9 +488,12 @@ hipError_t run(const LinearQ8& p, hipStream_t stream) {
     const auto tiles = [&](int bm, int bn) { return avae::tiles(p.M, p.N, bm, bn); };
     // (offsets inside a tile are 32 bits)
     if (by_rows(p.M, p.N) || p.lda >= (1 << 22) || p.ldw >= (1 << 22)) {
-        // the largest tiles that leave at least 144 workgroups
+        // the largest tiles that leave at least 144 workgroups, bfloat16:
         // ([37, 1536, 6144]: 16 x 16 12.1 us, 32 x 16 11.1, 32 x 32 13.8;
-        // [37, 6144, 1536]: 16 x 16 10.9, 32 x 16 9.6, 64 x 32 6.7)
+        // [37, 6144, 1536]: 16 x 16 10.9, 32 x 16 9.6, 64 x 32 6.7; at the
+        // limit, K = 6144: [1, 4608] 144 workgroups of 16 x 32 8.9 against
+        // 9.8 of 16 x 16, [1, 4096] 128 of them 8.8 against 7.1; [64, 4608]
+        // 144 of 64 x 32 19.8 against 24.4, [64, 4096] 128 19.7 against 13.9)
         if (p.M > 32 && tiles(64, 32) >= 144) return run_rows<T, SILU, AL, 4, 2>(p, stream);
         if (p.M > 16 && tiles(32, 32) >= 144) return run_rows<T, SILU, AL, 2, 2>(p, stream);
         if (p.M > 16 && tiles(32, 16) >= 144) return run_rows<T, SILU, AL, 2, 1>(p, stream);

@@ -12,7 +12,7 @@
 //
 // HBM-bound: every element is read once and written once.  Measured:
 // [8192, 8192] bfloat16 with residual 90 us (5.2 TB/s; a plain copy reaches
-// 5.1 here), [6000, 1536] 13.4 us (4.8), one row of 1536 3.0 us, which is
+// 5.1 here), [6000, 1536] 13.4 us (4.8), one row of 1536 3.1 us, which is
 // two memory latencies and the reduction; the read-back of [8192, 8192]
 // 33 us (6.2 TB/s), of float32 rows of odd length 3.7 TB/s (their stores
 // straddle cache lines).
