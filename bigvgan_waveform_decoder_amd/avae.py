@@ -102,6 +102,15 @@ class avae_ragged(ctypes.Structure):
                 ("table_cols", c_int), ("seqs", c_int), ("total", c_int), ("max_rows", c_int)]
 
 
+class avae_rope(ctypes.Structure):
+    _fields_ = [("freq", P), ("rot", c_int), ("interleaved", c_int), ("amp", c_float)]
+
+
+class avae_attn_rules(ctypes.Structure):
+    _fields_ = [("cap", c_float), ("slopes", P), ("prefix", P), ("max_prefix", c_int),
+                ("tree", P), ("tree_ld", ctypes.c_longlong), ("tree_words", c_int)]
+
+
 _lib = None
 
 
@@ -224,6 +233,21 @@ def lib() -> ctypes.CDLL:
     L.avae_attn_q8.restype = c_int
     L.avae_attn_q8.argtypes = [P, LL, LL, c_int, c_int, P, P, P, c_int, c_float, c_int, c_int, P,
                                P, P, c_size_t, P]
+    L.avae_rope_freq.restype = c_int
+    L.avae_rope_freq.argtypes = [c_int, c_double, c_int, c_double, c_double, c_double, c_double, P,
+                                 P]
+    L.avae_qk_norm_rope.restype = c_int
+    L.avae_qk_norm_rope.argtypes = [P, LL, LL, c_int, P, P, LL, LL, c_int, P, c_int, c_int,
+                                    c_float, P, P, P, c_int, P, LL, LL, P, LL, LL, P]
+    L.avae_kv_write_rope_q8.restype = c_int
+    L.avae_kv_write_rope_q8.argtypes = [P, LL, LL, P, LL, LL, c_int, P, c_float, P, P, P, P, P]
+    L.avae_attn_rules_q8_workspace_bytes.restype = c_size_t
+    L.avae_attn_rules_q8_workspace_bytes.argtypes = [P, P, c_int, c_int, c_int, c_int, P]
+    L.avae_attn_rules_q8.restype = c_int
+    L.avae_attn_rules_q8.argtypes = [P, LL, LL, c_int, c_int, P, P, P, c_int, c_float, c_int,
+                                     c_int, P, P, P, P, c_size_t, P]
+    L.avae_tree_mask.restype = c_int
+    L.avae_tree_mask.argtypes = [P, P, c_int, P, LL, P, P]
     L.avae_profile_begin.restype = c_int
     L.avae_profile_begin.argtypes = [c_int]
     L.avae_profile_end.restype = c_int
@@ -898,11 +922,15 @@ class _Env:
         self.float32 = torch.float32
         self.codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
         self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.device = torch._C._cuda_getDevice
         self.norm, self.quant, self.dequant = (L.avae_rms_norm_q8, L.avae_quant_q8,
                                                L.avae_dequant_q8)
         self.linear, self.linear_ws = L.avae_linear_q8, L.avae_linear_q8_workspace_bytes
         self.write, self.read = L.avae_kv_write_q8, L.avae_kv_read_q8
         self.attn, self.attn_ws = L.avae_attn_q8, L.avae_attn_q8_workspace_bytes
+        self.qk, self.write_rope, self.tree = (L.avae_qk_norm_rope, L.avae_kv_write_rope_q8,
+                                               L.avae_tree_mask)
+        self.rules, self.rules_ws = L.avae_attn_rules_q8, L.avae_attn_rules_q8_workspace_bytes
 
     def vec(self, n, dtype, dev):
         return self.strided((n,), (1,), dtype=dtype, device=dev)
@@ -922,6 +950,18 @@ class _Env:
     def stream(self, t):
         """The raw stream to launch on: the current one of the tensor's device."""
         return self.raw_stream(t.get_device())
+
+    def launch(self, t, f, *args):
+        """f(*args, stream) on the current stream of the tensor's device,
+        which is made the current device meanwhile."""
+        dev = t.get_device()
+        if dev == self.device():
+            rc = f(*args, self.raw_stream(dev))
+        else:
+            with _torch().cuda.device(dev):
+                rc = f(*args, self.raw_stream(dev))
+        if rc:
+            _check(rc)
 
 
 _env: Optional[_Env] = None
@@ -1183,3 +1223,214 @@ def attn_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = None,
     if rc:
         _check(rc)
     return (out, lse) if return_lse else out
+
+
+ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+
+
+def rope_freq(rot: int, theta: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+              context: float = 4096.0, low: float = 1.0, high: float = 32.0):
+    """avae_rope_freq: (frequencies [rot / 2] float32 on the host, amp)."""
+    kind = ROPE_SCALING.get(scaling)
+    if kind is None:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}, got {scaling!r}")
+    freq, amp = np.empty(max(rot // 2, 1), np.float32), c_float()
+    _check(lib().avae_rope_freq(rot, theta, kind, factor, context, low, high, freq.ctypes.data,
+                                ctypes.addressof(amp)))
+    return freq, amp.value
+
+
+class Rope:
+    """What turns queries and keys (avae_rope): freq [rot / 2] float32 on the
+    device, radians a position.  Rope.of(rot, ..) takes rope_freq's."""
+
+    __slots__ = ("freq", "rot", "c", "ref")
+
+    def __init__(self, freq, interleaved: bool = False, amp: float = 1.0):
+        if freq.dim() != 1 or freq.shape[0] < 1:
+            raise ValueError(f"freq: expected [rot / 2], got {tuple(freq.shape)}")
+        p = _vec(freq, "freq", freq.shape[0], _q8().float32)
+        self.freq, self.rot = freq, 2 * freq.shape[0]
+        self.c = avae_rope(p, self.rot, 1 if interleaved else 0, amp)
+        self.ref = ctypes.addressof(self.c)
+
+    @classmethod
+    def of(cls, rot: int, interleaved: bool = False, device="cuda", **kw):
+        freq, amp = rope_freq(rot, **kw)
+        return cls(_torch().from_numpy(freq).to(device), interleaved, amp)
+
+
+def _rows_of(E, cu, lens, total: int, max_rows: Optional[int]):
+    """Sequences without a page table."""
+    seqs = lens.shape[0]
+    return avae_ragged(_vec(cu, "cu", seqs + 1, E.int32), _vec(lens, "lens", seqs, E.int32), None,
+                       0, 0, seqs, total,
+                       total if max_rows is None or max_rows > total else max_rows)
+
+
+def _on(dev: int, *tensors):
+    """Refuses tensors of another device than the first one's."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on device {t.get_device()} and on device {dev}")
+
+
+def qk_norm_rope(q, k, rope: Optional[Rope], q_weight=None, k_weight=None, eps: float = 1e-6,
+                 positions=None, cu=None, lens=None, max_rows: Optional[int] = None,
+                 inplace: bool = False, stream=None):
+    """avae_qk_norm_rope: q [tokens, q_heads, dim] and k [tokens, k_heads, dim]
+    (or None) -> both normed (with weights [dim]) and turned; k's place holds
+    None if k is None.  A token's position is positions [tokens] int32, else
+    its place as cu and lens say; one of the two is needed."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return qk_norm_rope(q, k, rope, q_weight, k_weight, eps, positions, cu, lens, max_rows,
+                                inplace)
+    E = _q8()
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [tokens, heads, dim], got {tuple(q.shape)}")
+    (total, heads, dim), dtype, dev = q.shape, q.dtype, q.device
+    code = E.code(dtype)
+    pq, q_tok, q_head = _heads(q, "q", None, dim)
+    _on(q.get_device(), k, q_weight, k_weight, positions, cu, lens, rope and rope.freq)
+    q_out = q if inplace else E.heads(total, heads, dim, dtype, dev)
+    qo_tok, qo_head, _ = q_out.stride()
+    pk = pko = k_out = None
+    k_heads = k_tok = k_head = ko_tok = ko_head = 0
+    if k is not None:
+        if k.dtype != dtype or k.dim() != 3 or k.shape[0] != total:
+            raise ValueError("q and k must have one dtype and as many tokens")
+        k_heads = k.shape[1]
+        pk, k_tok, k_head = _heads(k, "k", None, dim)
+        k_out = k if inplace else E.heads(total, k_heads, dim, dtype, dev)
+        pko = k_out.data_ptr()
+        ko_tok, ko_head, _ = k_out.stride()
+    if (cu is None) != (lens is None):
+        raise ValueError("cu and lens are given together or not at all")
+    rows = None if cu is None else _rows_of(E, cu, lens, total, max_rows)
+    E.launch(q, E.qk, pq, q_tok, q_head, heads,
+             None if q_weight is None else _vec(q_weight, "q_weight", dim, E.float32),
+             pk, k_tok, k_head, k_heads,
+             None if k_weight is None else _vec(k_weight, "k_weight", dim, E.float32), dim, code,
+             eps, None if rope is None else rope.ref,
+             None if positions is None else _vec(positions, "positions", total, E.int32),
+             None if rows is None else ctypes.addressof(rows), total, q_out.data_ptr(), qo_tok,
+             qo_head, pko, ko_tok, ko_head)
+    return q_out, k_out
+
+
+def kv_write_rope_q8(cache: KvCacheQ8, k, v, table, cu, lens, rope: Optional[Rope], k_weight=None,
+                     eps: float = 1e-6, positions=None, max_new: Optional[int] = None,
+                     stream=None):
+    """avae_kv_write_rope_q8: kv_write_q8 with the keys normed (with k_weight
+    [dim]) and turned on the way, by positions [tokens] int32 or their places."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return kv_write_rope_q8(cache, k, v, table, cu, lens, rope, k_weight, eps, positions,
+                                    max_new)
+    E = _q8()
+    total = k.shape[0]
+    if v.dtype != k.dtype or v.shape[0] != total:
+        raise ValueError("k and v must have one dtype and as many tokens")
+    _on(k.get_device(), cache.k, v, table, cu, lens, rope and rope.freq, k_weight, positions)
+    rows = _ragged(E, table, cu, lens, total, max_new)
+    E.launch(
+        k, E.write_rope, *_heads(k, "k", cache.heads, cache.dim),
+        *_heads(v, "v", cache.heads, cache.dim), E.code(k.dtype),
+        None if k_weight is None else _vec(k_weight, "k_weight", cache.dim, E.float32), eps,
+        None if rope is None else rope.ref,
+        None if positions is None else _vec(positions, "positions", total, E.int32),
+        cache.ref, ctypes.addressof(rows))
+
+
+def _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, causal, window, first, rules,
+                return_lse):
+    E = _q8()
+    dim, dtype, dev = cache.dim, q.dtype, q.device
+    code = E.code(dtype)
+    pq, tok, head = _heads(q, "q", None, dim)
+    total, heads, _ = q.shape
+    _on(q.get_device(), cache.k, table, cu, lens, first)
+    rows = _ragged(E, table, cu, lens, total, max_q)
+    pr, px = ctypes.addressof(rows), ctypes.addressof(rules)
+    if max_len is None:
+        max_len = rows.table_cols * cache.page
+    if rules.max_prefix < 0:
+        rules.max_prefix = max_len
+    out = E.heads(total, heads, dim, dtype, dev)
+    lse = E.mat(total, heads, E.float32, dev) if return_lse else None
+    need = E.rules_ws(cache.ref, pr, heads, code, max_len, window, px)
+    ws = E.vec(need, E.uint8, dev) if need else None
+    E.launch(q, E.rules, pq, tok, head, heads, code, cache.ref, pr,
+             None if first is None else _vec(first, "first", rows.seqs, E.int32), max_len,
+             dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, px,
+             out.data_ptr(), None if lse is None else lse.data_ptr(),
+             None if ws is None else ws.data_ptr(), need)
+    return (out, lse) if return_lse else out
+
+
+def attn_rules_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = None,
+                  max_len: Optional[int] = None, scale: Optional[float] = None,
+                  causal: bool = True, window: int = 0, first=None, cap: float = 0.0, slopes=None,
+                  prefix=None, max_prefix: Optional[int] = None, return_lse: bool = False,
+                  stream=None):
+    """avae_attn_rules_q8: attn_q8 with scores capped (cap > 0), biased by
+    distance (slopes [q_heads] float32), and the first prefix [seqs] int32
+    tokens in view of every row.  max_prefix: at least the longest prefix
+    (max_len if not given)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return attn_rules_q8(q, cache, table, cu, lens, max_q, max_len, scale, causal, window,
+                                 first, cap, slopes, prefix, max_prefix, return_lse)
+    E = _q8()
+    if max_prefix is not None and max_prefix < 0:
+        raise ValueError(f"max_prefix is not negative, got {max_prefix}")
+    _on(q.get_device(), slopes, prefix)
+    rules = avae_attn_rules(
+        cap, None if slopes is None else _vec(slopes, "slopes", q.shape[1], E.float32),
+        None if prefix is None else _vec(prefix, "prefix", lens.shape[0], E.int32),
+        -1 if max_prefix is None else max_prefix, None, 0, 0)
+    return _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, causal, window, first,
+                       rules, return_lse)
+
+
+def tree_mask(parents, cu, lens, max_rows: Optional[int] = None, stream=None):
+    """avae_tree_mask: parents [tokens] int32 -> (mask [tokens, words] int32
+    with a bit for each draft that a draft sees, positions [tokens] int32).
+    max_rows: at least the most drafts of one sequence (all of them if not
+    given); the mask has a word for every 32 of them."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return tree_mask(parents, cu, lens, max_rows)
+    E = _q8()
+    if parents.dim() != 1:
+        raise ValueError(f"parents: expected [tokens], got {tuple(parents.shape)}")
+    total = parents.shape[0]
+    p = _vec(parents, "parents", total, E.int32)
+    _on(parents.get_device(), cu, lens)
+    rows = _rows_of(E, cu, lens, total, max_rows)
+    words = (rows.max_rows + 31) // 32
+    mask = E.mat(total, words, E.int32, parents.device)
+    positions = E.vec(total, E.int32, parents.device)
+    E.launch(parents, E.tree, p, ctypes.addressof(rows), words, mask.data_ptr(), words,
+             positions.data_ptr())
+    return mask, positions
+
+
+def attn_tree_q8(q, cache: KvCacheQ8, table, cu, lens, tree, max_q: Optional[int] = None,
+                 max_len: Optional[int] = None, scale: Optional[float] = None, first=None,
+                 cap: float = 0.0, return_lse: bool = False, stream=None):
+    """avae_attn_rules_q8 over a tree of drafts: each row sees what lies before
+    its sequence's rows, and of those rows the ones that its mask in tree
+    [tokens, words] int32 has bits for (tree_mask makes it)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return attn_tree_q8(q, cache, table, cu, lens, tree, max_q, max_len, scale, first, cap,
+                                return_lse)
+    E = _q8()
+    total, words = q.shape[0], _two_axes(tree, "tree")[1]
+    p, ld = _rows(tree, "tree", E.int32, total, words)
+    _on(q.get_device(), tree)
+    rules = avae_attn_rules(cap, None, None, 0, p, ld, words)
+    return _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, True, 0, first, rules,
+                       return_lse)

@@ -180,6 +180,34 @@ hipError_t launch_kv_write_q8(int dtype, const void* k, long long k_tok, long lo
 hipError_t launch_kv_read_q8(int dtype, const CacheQ8& c, const Ragged& r, void* k, void* v,
                              hipStream_t stream);
 
+// What turns the heads.  positions null: a row's place in its sequence.
+struct RopeQ8 {
+    const float* freq;     // [half] radians a position
+    int half;              // pairs that are turned
+    int apart;             // half where the dims of a pair are that far apart, 0: neighbours
+    float amp;
+    const int* positions;  // [total]
+};
+
+// Heads x [total][heads][dim] that go to y, at their strides; weight [dim]
+// null: no norm.
+struct HeadsQ8 {
+    const void* x;
+    void* y;
+    const float* weight;
+    long long tok, head, y_tok, y_head;
+    int heads;
+};
+// r.cu null: all r.total rows (positions given).
+hipError_t launch_qk_norm_rope(int dtype, const HeadsQ8& q, const HeadsQ8& k, const RopeQ8& rope,
+                               const Ragged& r, int dim, float eps, hipStream_t stream);
+hipError_t launch_kv_write_rope_q8(int dtype, const void* k, long long k_tok, long long k_head,
+                                   const void* v, long long v_tok, long long v_head,
+                                   const float* weight, float eps, const RopeQ8& rope,
+                                   const CacheQ8& c, const Ragged& r, hipStream_t stream);
+hipError_t launch_tree_mask(const int* parents, const Ragged& r, int words, int* mask,
+                            long long ld, int* positions, hipStream_t stream);
+
 struct AttnQ8 {
     const void* q;            // [total][q_heads][dim], strides q_tok, q_head
     long long q_tok, q_head;
@@ -189,12 +217,26 @@ struct AttnQ8 {
     int q_heads, max_len, causal, window;
     float scale;
 };
+// prefix: tokens in view whatever the window, at most (0 without a window).
 size_t attn_q8_workspace_bytes(int seqs, int total, int max_rows, int max_len, int q_heads,
-                               int heads, int dim, int elem, int window);
+                               int heads, int dim, int elem, int window, int prefix = 0);
 // Workgroups of 256 threads that the largest of its launches has.
 long long attn_q8_workgroups(int seqs, int total, int max_rows, int max_len, int q_heads,
-                             int heads, int dim, int elem, int window);
+                             int heads, int dim, int elem, int window, int prefix = 0);
 hipError_t launch_attn_q8(int dtype, const AttnQ8& a, const CacheQ8& c, const Ragged& r, void* ws,
                           hipStream_t stream);
+
+// What the attention does to its scores, and which keys a row sees besides.
+struct AttnRules {
+    float cap;              // 0: none
+    const float* slopes;    // [q_heads] or null
+    const int* prefix;      // [seqs] or null
+    int max_prefix;
+    const unsigned* tree;   // [total][tree_words] bits at stride tree_ld, or null
+    long long tree_ld;
+    int tree_words;
+};
+hipError_t launch_attn_rules_q8(int dtype, const AttnQ8& a, const AttnRules& x, const CacheQ8& c,
+                                const Ragged& r, void* ws, hipStream_t stream);
 
 }  // namespace avae

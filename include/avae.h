@@ -658,6 +658,140 @@ int avae_attn_q8(const void* q, long long q_tok, long long q_head, int q_heads, 
                  size_t ws_bytes, void* stream);
 
 /*
+ * Rotary positions.  The first `rot` dims of a head are rot / 2 pairs (a, b):
+ * dims (i, i + rot / 2), or (2 i, 2 i + 1) if `interleaved`.  At position p
+ * pair i is turned by the angle p * freq[i]:
+ *   a' = amp (a cos - b sin),  b' = amp (b cos + a sin);
+ * the other dims stay.  The angle is taken in 64 bits: right to float32's
+ * rounding for positions below 2^24 and frequencies up to 1, and to 2e-7 for
+ * any below 2^29.
+ *   freq: DEVICE, [rot / 2] float32, radians a position, up to 2^16; rot:
+ *   even, 0 (nothing is turned) up to the head's dims; amp: finite.
+ */
+typedef struct avae_rope {
+    const float* freq;
+    int rot;
+    int interleaved;
+    float amp;
+} avae_rope;
+
+/*
+ * Frequencies for avae_rope, f_i = theta^(-2 i / rot), scaled for contexts
+ * `factor` times as long as the trained one:
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor
+ *   BASE    f_i of the base theta * factor^(rot / (rot - 2))
+ *   BANDS   f_i * w + f_i / factor * (1 - w), w = (turns - low) / (high - low)
+ *           in 0 .. 1, turns = context * f_i / 2 pi: what a pair turns over
+ *           the trained context
+ *   RAMP    the same with w falling linearly in i from the pair that turns
+ *           `high` times (rounded down) to the one that turns `low` times
+ *           (rounded up); amp becomes 0.1 ln(factor) + 1 (else 1)
+ *   freq [rot / 2], amp [1]: HOST memory.  context, low, high: read by the
+ *   last two, 0 < low < high.
+ * Errors: EINVAL, ESHAPE (rot not even or not in 2 .. 65536; BASE with rot 2).
+ */
+enum avae_rope_scaling {
+    AVAE_ROPE_PLAIN = 0,
+    AVAE_ROPE_LINEAR = 1,
+    AVAE_ROPE_BASE = 2,
+    AVAE_ROPE_BANDS = 3,
+    AVAE_ROPE_RAMP = 4
+};
+int avae_rope_freq(int rot, double theta, int scaling, double factor, double context, double low,
+                   double high, float* freq, float* amp);
+
+/*
+ * Queries and keys normed for each head and turned by their positions, in one
+ * pass.  With a weight a head x becomes
+ *   x / sqrt(mean_d(x^2) + eps) * weight
+ * (a head of zeros stays zeros whatever eps is; 64 bits where the squares
+ * leave float32), without one it is taken as it is; then it is turned.  All
+ * in float32, rounded to dtype once.
+ *   q: [total, q_heads, dim] of dtype at strides q_tok, q_head; q_out: the
+ *   same at its own strides.  k likewise; k_heads 0: queries alone, k is not
+ *   read.  q_weight, k_weight: [dim] float32 or NULL.  An output may be its
+ *   input (with its strides), and overlap nothing else.
+ *   dim: even, 2 .. 512.  rope: NULL turns nothing.
+ *   positions: [total] int32, or NULL: a row's place in its sequence,
+ *   lens[b] - (cu[b+1] - cu[b]) + i for row cu[b] + i.
+ *   rows: cu, lens and sizes (no table); rows of no sequence stay as they
+ *   were.  NULL: all `total` rows, and positions are given.
+ * Errors: EINVAL, ESHAPE.
+ */
+int avae_qk_norm_rope(const void* q, long long q_tok, long long q_head, int q_heads,
+                      const float* q_weight, const void* k, long long k_tok, long long k_head,
+                      int k_heads, const float* k_weight, int dim, int dtype, float eps,
+                      const avae_rope* rope, const int* positions, const avae_ragged* rows,
+                      int total, void* q_out, long long qo_tok, long long qo_head, void* k_out,
+                      long long ko_tok, long long ko_head, void* stream);
+
+/*
+ * avae_kv_write_q8 with the keys normed and turned on the way, as
+ * avae_qk_norm_rope does it but kept in float32 up to the quantiser: the
+ * scales are of the turned keys.  Values are written as they are.
+ *   k_weight: [dim] float32 or NULL (no norm); rope: NULL turns nothing;
+ *   positions: [total] int32 or NULL (a token's place).  Where a token is
+ *   written goes by cu and lens alone: drafts of one position take several
+ *   places.
+ * Errors: EINVAL, ESHAPE.
+ */
+int avae_kv_write_rope_q8(const void* k, long long k_tok, long long k_head, const void* v,
+                          long long v_tok, long long v_head, int dtype, const float* k_weight,
+                          float eps, const avae_rope* rope, const int* positions,
+                          const avae_kv_q8* cache, const avae_ragged* rows, void* stream);
+
+/*
+ * Attention over the cache as avae_attn_q8 (every argument of its is the same
+ * here, and so is what it says of precision and NaN), with rules:
+ *   cap > 0: scores become cap * tanh(score / cap).
+ *   slopes [q_heads] float32 or NULL: then slope * |p - t| is taken off the
+ *     score of key t for the row at place p.  Finite, of either sign.
+ *   prefix [seqs] int32 or NULL (causal only): keys t < prefix[b] are seen by
+ *     every row of sequence b, whatever its place and the window are: with a
+ *     window those keys and the window's.  max_prefix: at least the largest
+ *     of them (longer ones are cut to it).
+ *   tree or NULL: the rows are drafts that follow one another as a tree: row
+ *     i of a sequence sees the tokens before its first row, and of the
+ *     sequence's rows those j whose bit (word j / 32, bit j % 32) is set in
+ *     its own mask, [total, tree_words] at row stride tree_ld: itself too
+ *     only if its bit is set.  Goes with causal attention and first, not
+ *     with window, slopes or prefix.  At most AVAE_TREE_MAX_WORDS words.
+ * first hides keys from all of this.  A row before its sequence's first token
+ * (more rows than tokens) sees nothing.
+ * Errors: as avae_attn_q8; EINVAL (cap not 0 and not in 1e-30 .. 1e30, rules
+ *   that do not go together), ESHAPE (a mask too small for max_rows).
+ *
+ * avae_tree_mask makes such masks from parents: parents[cu[b] + i] is the
+ *   place among the sequence's rows that row i follows, below i; anything
+ *   else follows the token before the sequence's rows.  mask: [total, words]
+ *   at row stride ld, every word of a row written; positions: [total] int32
+ *   or NULL: the token's position, places before the rows plus its depth in
+ *   the tree.  rows: as avae_qk_norm_rope's.
+ */
+#define AVAE_TREE_MAX_WORDS 128
+typedef struct avae_attn_rules {
+    float cap;
+    const float* slopes;
+    const int* prefix;
+    int max_prefix;
+    const int* tree;
+    long long tree_ld;
+    int tree_words;
+} avae_attn_rules;
+
+size_t avae_attn_rules_q8_workspace_bytes(const avae_kv_q8* cache, const avae_ragged* rows,
+                                          int q_heads, int dtype, int max_len, int window,
+                                          const avae_attn_rules* rules);
+int avae_attn_rules_q8(const void* q, long long q_tok, long long q_head, int q_heads, int dtype,
+                       const avae_kv_q8* cache, const avae_ragged* rows, const int* first,
+                       int max_len, float scale, int causal, int window,
+                       const avae_attn_rules* rules, void* out, float* lse, void* workspace,
+                       size_t ws_bytes, void* stream);
+int avae_tree_mask(const int* parents, const avae_ragged* rows, int words, int* mask, long long ld,
+                   int* positions, void* stream);
+
+/*
  * Launch profiler, the device-side counterpart of the audio decoder's own
  * phase report ([H3] AVAE_TIME / avae_time_report, phases dec_in, conv_pre,
  * upsamples, resblocks, act_post, conv_post).  Between avae_profile_begin and
