@@ -273,7 +273,7 @@ extern "C" size_t avae_attn_q8_workspace_bytes(const avae_kv_q8* cache, const av
 static int check_attn(const char* who, const void* q, long long q_tok, long long q_head,
                       int q_heads, int dtype, const avae_kv_q8* cache, const avae_ragged* rows,
                       const int* first, int max_len, float scale, int causal, int window,
-                      int prefix, void* out, float* lse, void* workspace, size_t ws_bytes,
+                      int prefix, bool rules, void* out, float* lse, void* workspace, size_t ws_bytes,
                       avae::AttnQ8* to, CacheQ8* cache_to, Ragged* rows_to, bool* nothing) {
     CacheQ8& c = *cache_to;
     Ragged& r = *rows_to;
@@ -310,13 +310,13 @@ static int check_attn(const char* who, const void* q, long long q_tok, long long
     AVAE_CHECK(check_strides(who, "q", q_tok, q_head, r.total, q_heads, c.dim));
     const size_t need = avae::attn_q8_workspace_bytes(r.seqs, r.total, r.max_rows, max_len, q_heads,
                                                       c.heads, c.dim, elem_size(dtype), window,
-                                                      prefix);
+                                                      prefix, rules);
     if (need && (!workspace || ws_bytes < need || misaligned(workspace, 16)))
         return abi_fail(AVAE_EWORKSPACE, "%s: %zu bytes of workspace, aligned to 16, are needed",
                         who, need);
     const long long groups = avae::attn_q8_workgroups(
         r.seqs, r.total, r.max_rows, max_len, q_heads, c.heads, c.dim, elem_size(dtype), window,
-        prefix);
+        prefix, rules);
     if (groups > kMaxGroups)
         return abi_fail(AVAE_ESHAPE,
                         "%s: %d sequences of up to %d rows are %lld workgroups, over 2^24: give the "
@@ -349,7 +349,7 @@ extern "C" int avae_attn_q8(const void* q, long long q_tok, long long q_head, in
     Ragged r;
     bool nothing = false;
     AVAE_CHECK(check_attn(who, q, q_tok, q_head, q_heads, dtype, cache, rows, first, max_len, scale,
-                          causal, window, 0, out, lse, workspace, ws_bytes, &a, &c, &r, &nothing));
+                          causal, window, 0, false, out, lse, workspace, ws_bytes, &a, &c, &r, &nothing));
     if (nothing) return AVAE_OK;
     return done(avae::launch_attn_q8(dtype, a, c, r, workspace, (hipStream_t)stream), who);
 }
@@ -555,7 +555,7 @@ extern "C" size_t avae_attn_rules_q8_workspace_bytes(const avae_kv_q8* cache,
         return 0;
     return avae::attn_q8_workspace_bytes(rows->seqs, rows->total, rows->max_rows, max_len, q_heads,
                                          cache->heads, cache->dim, elem_size(dtype), window,
-                                         prefix_of(rules));
+                                         prefix_of(rules), true);
 }
 
 extern "C" int avae_attn_rules_q8(const void* q, long long q_tok, long long q_head, int q_heads,
@@ -590,10 +590,11 @@ extern "C" int avae_attn_rules_q8(const void* q, long long q_tok, long long q_he
     Ragged r;
     bool nothing = false;
     AVAE_CHECK(check_attn(who, q, q_tok, q_head, q_heads, dtype, cache, rows, first, max_len, scale,
-                          causal, window, prefix_of(rules), out, lse, workspace, ws_bytes, &a, &c,
+                          causal, window, prefix_of(rules), true, out, lse, workspace, ws_bytes, &a, &c,
                           &r, &nothing));
     if (nothing) return AVAE_OK;
     const avae::AttnRules x{rules->cap, rules->slopes, rules->prefix, rules->max_prefix,
-                            (const unsigned*)rules->tree, rules->tree_ld, rules->tree_words};
+                            (const unsigned*)rules->tree, rules->tree_ld, rules->tree_words, 0,
+                            0};
     return done(avae::launch_attn_rules_q8(dtype, a, x, c, r, workspace, (hipStream_t)stream), who);
 }

@@ -219,10 +219,12 @@ struct AttnQ8 {
 };
 // prefix: tokens in view whatever the window, at most (0 without a window).
 size_t attn_q8_workspace_bytes(int seqs, int total, int max_rows, int max_len, int q_heads,
-                               int heads, int dim, int elem, int window, int prefix = 0);
+                               int heads, int dim, int elem, int window, int prefix = 0,
+                               bool rules = false);
 // Workgroups of 256 threads that the largest of its launches has.
 long long attn_q8_workgroups(int seqs, int total, int max_rows, int max_len, int q_heads,
-                             int heads, int dim, int elem, int window, int prefix = 0);
+                             int heads, int dim, int elem, int window, int prefix = 0,
+                             bool rules = false);
 hipError_t launch_attn_q8(int dtype, const AttnQ8& a, const CacheQ8& c, const Ragged& r, void* ws,
                           hipStream_t stream);
 
@@ -235,6 +237,7 @@ struct AttnRules {
     const unsigned* tree;   // [total][tree_words] bits at stride tree_ld, or null
     long long tree_ld;
     int tree_words;
+    int pieces, span;       // set by the launch: how the keys of many rows are cut
 };
 hipError_t launch_attn_rules_q8(int dtype, const AttnQ8& a, const AttnRules& x, const CacheQ8& c,
                                 const Ragged& r, void* ws, hipStream_t stream);

@@ -214,21 +214,41 @@ template <typename T>
 struct Shape {
     float cap, slope;  // in units of log2 e; the slope is the row's
     bool capped, sloped;
+    // 16-bit types: cap tanh(y) = cap - 2 cap / (1 + exp(2 y)), the first term
+    // left out of the scores since all of a row have it; 5 2^-24 cap off,
+    // which for caps up to 256 their own rounding hides.
+    bool quick;
 
     __device__ Shape(const AttnRules& x, const Row& r)
-        : cap(x.cap * kLog2e), slope(0.0f), capped(x.cap > 0.0f), sloped(x.slopes != nullptr) {
+        : cap(x.cap * kLog2e), slope(0.0f), capped(x.cap > 0.0f), sloped(x.slopes != nullptr),
+          quick(sizeof(T) < 4 && x.cap > 0.0f && x.cap <= 256.0f) {
         if (sloped) slope = x.slopes[r.q_head] * kLog2e;
     }
     // (a scale that is not finite stays with the score whatever the cap)
     __device__ float by(float ks, float to_log2) const {
         return finite(ks) ? ks * to_log2 : nan();
     }
-    __device__ float operator()(float s, int distance) const {
-        if (capped) s = cap * tanh_of<T>(s);
-        if (sloped) s = fmaf(-slope, (float)abs(distance), s);
-        return s;
+    // The cap,
+    // of s = 2 y log2 e, over 2 cap
+    __device__ float cap_quick(float s) const {
+        return __builtin_amdgcn_rcpf(-1.0f - __builtin_amdgcn_exp2f(s));
+    }
+    // of s = y
+    __device__ float cap_whole(float s) const { return cap * tanh_of<T>(s); }
+    // The bias of a key that far away (past 2^24 to float32's rounding).
+    __device__ float bend(float s, float distance) const {
+        return fmaf(-slope, fabsf(distance), s);
     }
 };
+
+template <typename T>
+__device__ inline Shape<T> shape_of(const AttnRules& x, const Row& r) {
+    return Shape<T>(x, r);
+}
+template <typename T>
+__device__ inline NoRules shape_of(const NoRules&, const Row&) {
+    return {};
+}
 
 // Smallest and largest key bounds of a tile's rows that see any key, over
 // the 16 lanes of each group; no row sees all keys from `whole` on.
@@ -390,6 +410,7 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
     if constexpr (kRules<R>)
         if (x.cap > 0.0f) to_log2 = q.back * (a.scale / x.cap);
 
+    const auto shape = shape_of<T>(x, row);
     f4 acc[DT] = {};
     // v_run: the largest value scale so far, the accumulated values' unit; at
     // least float32's smallest normal number, which has a reciprocal
@@ -438,11 +459,17 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
                 }
             }
             if constexpr (kRules<R>) {
-                const Shape<T> shape(x, row);
-                sum *= shape.by(ks[h], to_log2);
+                const float by = shape.capped ? shape.by(ks[h], to_log2) : ks[h] * to_log2;
+                s[h] = sum * by;
+                if (shape.capped) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[h][i] = shape(sum[i], row.pos - (t0 + 16 * h + 4 * g + i));
+                    for (int i = 0; i < 4; ++i) s[h][i] = shape.cap_whole(s[h][i]);
+                }
+                if (shape.sloped) {
+                    const float away = (float)(row.pos - (t0 + 16 * h + 4 * g));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[h][i] = shape.bend(s[h][i], away - i);
+                }
             } else {
                 s[h] = sum * (ks[h] * to_log2);
             }
@@ -631,6 +658,20 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
     if (!ragged_rows(r, b, cu0, n, len)) return;
     const int group = a.q_heads / c.heads, rows = n * group, r0 = tile * HEIGHT;
     if (r0 >= rows) return;
+    if constexpr (kRules<R>)
+        if (x.pieces) {
+            // as in the kernel for few rows: chunks by what there is in all
+            long long keys = 0;
+            for (int i = lane; i < r.seqs; i += 64) {
+                int at, count, length;
+                if (ragged_rows(r, i, at, count, length))
+                    keys += (long long)min(length, x.span) * ((count * group - 1) / HEIGHT + 1);
+            }
+            for (int o = 32; o > 0; o >>= 1) keys += __shfl_xor(keys, o);
+            const long long even = (keys * c.heads + x.pieces - 1) / x.pieces;
+            const int least = (x.span + splits - 1) / splits;
+            chunk = (min(chunk, max((int)min(even, (long long)chunk), least)) + 63) & ~63;
+        }
     // keys that any of the workgroup's rows sees; bounds grow with the row
     const Row row1 = row_of(a, c, x, b, head, cu0, n, len, min(r0 + HEIGHT - 1, rows - 1));
     const int first = a.first ? max(a.first[b], 0) : 0;
@@ -765,6 +806,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
         s_group[lane == 0 ? buf : 2 + (lane >> 2)][lane == 0 ? wave : lane & 3] = to;
     };
 
+    const auto shape = shape_of<T>(x, row);
     f16v acc[DT] = {};
     float m = neg_inf(), l = 0.0f;
     // The accumulated values are in units of 2^(lg_run - 15), lg_run the
@@ -847,6 +889,16 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
         }
     };
 
+    if constexpr (kRules<R>)
+        if (splits > 1 && t_lo >= t_hi) {  // a chunk without keys
+            if (row.live && g == 0) {
+                float* pr =
+                    part + (((long long)row.tok * a.q_heads + row.q_head) * splits + split) * (D + 4);
+                pr[0] = neg_inf();
+                pr[1] = 0.0f;
+            }
+            return;
+        }
     if (t_lo < t_hi) {
         look_up(key_at(t_lo));
         fetch(key_at(t_lo));
@@ -889,17 +941,47 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
                         fetch(key_at(u0 + 128));  // a step's time to arrive
                     }
                     if constexpr (kRules<R>) {
-                        const Shape<T> shape(x, row);
+                        if (shape.capped) {
 #pragma unroll
-                        for (int h = 0; h < HS; ++h)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const int t = t0 + 32 * (h0 + h) + 4 * g + 8 * (j >> 2) + (j & 3);
-                                const Group& gr = gp[2 * (h0 + h) + j / 8];
-                                s[h][j] = shape(s[h][j] * shape.by(gr.ks, to_log2), row.pos - t);
+                            for (int u = 0; u < 2 * HS; ++u) {
+                                const float to = shape.by(gp[2 * h0 + u].ks, to_log2);
+                                by[u] = shape.quick ? to * (2.0f * kLog2e) : to;
                             }
+                        }
+                        if (shape.quick) {
 #pragma unroll
-                        for (int u = 0; u < 2 * HS; ++u) by[u] = 1.0f;
+                            for (int u = 0; u < 2 * HS; ++u) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const int i = u % 2 * 8 + j;
+                                    s[u / 2][i] = shape.cap_quick(s[u / 2][i] * by[u]);
+                                }
+                                by[u] = 2.0f * shape.cap;
+                            }
+                        } else if (shape.capped) {
+#pragma unroll
+                            for (int u = 0; u < 2 * HS; ++u) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const int i = u % 2 * 8 + j;
+                                    s[u / 2][i] = shape.cap_whole(s[u / 2][i] * by[u]);
+                                }
+                                by[u] = 1.0f;
+                            }
+                        }
+                        if (shape.sloped) {
+                            const float away = (float)(row.pos - (t0 + 32 * h0 + 4 * g));
+#pragma unroll
+                            for (int u = 0; u < 2 * HS; ++u) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const int i = u % 2 * 8 + j;
+                                    const float at = away - (16 * u + 8 * (j >> 2) + (j & 3));
+                                    s[u / 2][i] = shape.bend(s[u / 2][i] * by[u], at);
+                                }
+                                by[u] = 1.0f;
+                            }
+                        }
                     }
                     if (!seen) {
                         // What is hidden from a row goes into its scores, and
@@ -952,6 +1034,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
 
     l = (l + __shfl_xor(l, 32)) * 0x1p-15f;
     if (!row.live) return;
+    if constexpr (kRules<R>)
+        if (shape.quick) m += shape.cap;
     const long long out_row = (long long)row.tok * a.q_heads + row.q_head;
     // the unit in two halves, since it may be below float32
     const float half = __builtin_amdgcn_exp2f(0.5f * (lg_run - 15.0f));
@@ -1110,7 +1194,7 @@ struct Cut {
 inline int round_up_to(long long x, int step) { return (int)((x + step - 1) / step * step); }
 
 inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int dim, int elem,
-               int window, int prefix) {
+               int window, int prefix, bool rules) {
     const int group = q_heads / heads;
     const long long rows = (long long)max_rows * group;
     Cut r;
@@ -1128,7 +1212,12 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
             r.span, (long long)window + height / group + 65 + (prefix > 0 ? prefix + 126LL : 0));
     const long long pairs = (long long)seqs * heads * r.tiles;
     r.pieces = 0;
-    if (r.many) {
+    if (r.many && rules && r.tiles <= 4) {
+        // Drafts over long sequences
+        const int resident = 512;
+        r.chunk = std::max(round_up_to((r.span * pairs + resident - 1) / resident, step), 256);
+        if (seqs > 1 && seqs <= 1024) r.pieces = resident;
+    } else if (r.many) {
         // Split only to give every CU a workgroup, in chunks of 128 keys or
         // more: the joined parts are float32 rows ([4 x 512 rows, 1000 keys,
         // 12 heads], 192 workgroups: 43 us whole, 52 in two parts; [5 x 17
@@ -1155,13 +1244,17 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
 inline bool join_by_waves(int splits, long long rows) { return splits <= 64 && rows >= 2048; }
 
 template <typename T, int D, typename R>
-hipError_t run(const AttnQ8& a, const R& x, const CacheQ8& c, const Ragged& r, float* part,
+hipError_t run(const AttnQ8& a, R x, const CacheQ8& c, const Ragged& r, float* part,
                hipStream_t stream) {
     int prefix = 0;
     if constexpr (kRules<R>) prefix = x.prefix ? x.max_prefix : 0;
-    const Cut k =
-        cut(r.seqs, r.max_rows, a.max_len, a.q_heads, c.heads, D, sizeof(T), a.window, prefix);
+    const Cut k = cut(r.seqs, r.max_rows, a.max_len, a.q_heads, c.heads, D, sizeof(T), a.window,
+                      prefix, kRules<R>);
     const long long blocks = (long long)k.tiles * k.splits * c.heads * r.seqs;
+    if constexpr (kRules<R>) {
+        x.pieces = k.pieces;
+        x.span = k.span;
+    }
     if (k.many)
         hipLaunchKernelGGL((attn_q8_many_kernel<T, D, R>),
                            dim3((unsigned)blocks),

@@ -4,14 +4,16 @@
 namespace avae {
 
 size_t attn_q8_workspace_bytes(int seqs, int total, int max_rows, int max_len, int q_heads,
-                               int heads, int dim, int elem, int window, int prefix) {
-    const Cut k = cut(seqs, max_rows, max_len, q_heads, heads, dim, elem, window, prefix);
+                               int heads, int dim, int elem, int window, int prefix,
+                               bool rules) {
+    const Cut k = cut(seqs, max_rows, max_len, q_heads, heads, dim, elem, window, prefix, rules);
     return k.splits > 1 ? (size_t)total * q_heads * k.splits * (dim + 4) * sizeof(float) : 0;
 }
 
 long long attn_q8_workgroups(int seqs, int total, int max_rows, int max_len, int q_heads,
-                             int heads, int dim, int elem, int window, int prefix) {
-    const Cut k = cut(seqs, max_rows, max_len, q_heads, heads, dim, elem, window, prefix);
+                             int heads, int dim, int elem, int window, int prefix,
+                             bool rules) {
+    const Cut k = cut(seqs, max_rows, max_len, q_heads, heads, dim, elem, window, prefix, rules);
     const long long blocks = (long long)k.tiles * k.splits * heads * seqs;
     const long long rows = (long long)total * q_heads;
     if (k.splits == 1) return blocks;
