@@ -459,8 +459,7 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
                 }
             }
             if constexpr (kRules<R>) {
-                const float by = shape.capped ? shape.by(ks[h], to_log2) : ks[h] * to_log2;
-                s[h] = sum * by;
+                s[h] = sum * shape.by(ks[h], to_log2);
                 if (shape.capped) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s[h][i] = shape.cap_whole(s[h][i]);
@@ -607,6 +606,75 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
 
 typedef float f16v __attribute__((ext_vector_type(16)));
 
+// Scores of 32 keys by the rules, as the exponential takes them: s * by, a
+// factor for each 16.  `away`: the row's distance from the lane's first key.
+template <typename T>
+__device__ inline void shape_scores(const Shape<T>& shape, f16v& s, float* by, float away) {
+    if (shape.quick) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            by[u] *= 2.0f * kLog2e;
+#pragma unroll
+            for (int j = 8 * u; j < 8 * u + 8; ++j) s[j] = shape.cap_quick(s[j] * by[u]);
+            by[u] = 2.0f * shape.cap;
+        }
+    } else if (shape.capped) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int j = 8 * u; j < 8 * u + 8; ++j) s[j] = shape.cap_whole(s[j] * by[u]);
+            by[u] = 1.0f;
+        }
+    }
+    if (shape.sloped) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int j = 8 * u; j < 8 * u + 8; ++j)
+                s[j] = shape.bend(s[j] * by[u], away - (8 * (j >> 2) + (j & 3)));
+            by[u] = 1.0f;
+        }
+    }
+}
+
+// The chunk of keys by which a launch's sequences are cut: the host knows
+// only the longest one and left room for `splits` chunks of it; each lane
+// tries another chunk that this room allows, and the one whose pieces are done
+// first is taken, x.pieces of them at once and a start counted as kStart keys.
+constexpr int kStart = 256;
+
+__device__ inline int best_chunk(const AttnRules& x, const CacheQ8& c, const Ragged& r, int lane,
+                                 int group, int height, int splits, int step) {
+    const int least = ((x.span + splits - 1) / splits + step - 1) & ~(step - 1);
+    const int chunk = (least + (int)((long long)least * lane / 16) + step - 1) & ~(step - 1);
+    int at, count, length = 0, tiles = 0;
+    if (lane < r.seqs && ragged_rows(r, lane, at, count, length))
+        tiles = ((count * group - 1) / height + 1) * c.heads;
+    length = min(length, x.span);
+    const float whole = (float)(chunk + kStart), inv = 1.0f / (float)chunk;
+    // pieces of a whole chunk; all pieces; keys of those that are not whole
+    float full = 0.0f, all = 0.0f, rest = 0.0f;
+    for (int i = 0; i < r.seqs; ++i) {
+        const float keys = (float)__builtin_amdgcn_readlane(length, i);
+        const float times = (float)__builtin_amdgcn_readlane(tiles, i);
+        const float n = floorf(keys * inv), left = keys - n * (float)chunk;
+        full += times * n;
+        rest += left > 0.0f ? times * (left + (float)kStart) : 0.0f;
+        all += times * (left > 0.0f ? n + 1.0f : n);
+    }
+    // rounds of whole chunks with the rest beside them, or where that does
+    // not fit what there is in all and a part of a chunk, by which ends differ
+    const float at_once = 1.0f / (float)x.pieces;
+    const float rounds = fmaxf(ceilf(full * at_once), 1.0f);
+    float done = rounds * whole;
+    if (all > rounds * (float)x.pieces)
+        done = fmaxf(done, (full * whole + rest) * at_once + 0.25f * (float)chunk);
+    // (positive: as bits in order; the lane in the last six, so that all agree)
+    unsigned cost = (__float_as_uint(done) & ~63u) | (unsigned)lane;
+    for (int o = 32; o > 0; o >>= 1) cost = min(cost, (unsigned)__shfl_xor((int)cost, o));
+    return __builtin_amdgcn_readlane(chunk, __builtin_amdgcn_readfirstlane((int)(cost & 63u)));
+}
+
 // 16 keys of one page: their scales, as the softmax takes them.
 struct alignas(16) Group {
     float ks, vs, lg_vs;  // staged: vs is 1 / the value scale, lg_vs its logarithm
@@ -659,19 +727,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
     const int group = a.q_heads / c.heads, rows = n * group, r0 = tile * HEIGHT;
     if (r0 >= rows) return;
     if constexpr (kRules<R>)
-        if (x.pieces) {
-            // as in the kernel for few rows: chunks by what there is in all
-            long long keys = 0;
-            for (int i = lane; i < r.seqs; i += 64) {
-                int at, count, length;
-                if (ragged_rows(r, i, at, count, length))
-                    keys += (long long)min(length, x.span) * ((count * group - 1) / HEIGHT + 1);
-            }
-            for (int o = 32; o > 0; o >>= 1) keys += __shfl_xor(keys, o);
-            const long long even = (keys * c.heads + x.pieces - 1) / x.pieces;
-            const int least = (x.span + splits - 1) / splits;
-            chunk = (min(chunk, max((int)min(even, (long long)chunk), least)) + 63) & ~63;
-        }
+        if (x.pieces) chunk = best_chunk(x, c, r, lane, group, HEIGHT, splits, 64);
     // keys that any of the workgroup's rows sees; bounds grow with the row
     const Row row1 = row_of(a, c, x, b, head, cu0, n, len, min(r0 + HEIGHT - 1, rows - 1));
     const int first = a.first ? max(a.first[b], 0) : 0;
@@ -941,46 +997,12 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
                         fetch(key_at(u0 + 128));  // a step's time to arrive
                     }
                     if constexpr (kRules<R>) {
-                        if (shape.capped) {
 #pragma unroll
-                            for (int u = 0; u < 2 * HS; ++u) {
-                                const float to = shape.by(gp[2 * h0 + u].ks, to_log2);
-                                by[u] = shape.quick ? to * (2.0f * kLog2e) : to;
-                            }
-                        }
-                        if (shape.quick) {
-#pragma unroll
-                            for (int u = 0; u < 2 * HS; ++u) {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const int i = u % 2 * 8 + j;
-                                    s[u / 2][i] = shape.cap_quick(s[u / 2][i] * by[u]);
-                                }
-                                by[u] = 2.0f * shape.cap;
-                            }
-                        } else if (shape.capped) {
-#pragma unroll
-                            for (int u = 0; u < 2 * HS; ++u) {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const int i = u % 2 * 8 + j;
-                                    s[u / 2][i] = shape.cap_whole(s[u / 2][i] * by[u]);
-                                }
-                                by[u] = 1.0f;
-                            }
-                        }
-                        if (shape.sloped) {
-                            const float away = (float)(row.pos - (t0 + 32 * h0 + 4 * g));
-#pragma unroll
-                            for (int u = 0; u < 2 * HS; ++u) {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const int i = u % 2 * 8 + j;
-                                    const float at = away - (16 * u + 8 * (j >> 2) + (j & 3));
-                                    s[u / 2][i] = shape.bend(s[u / 2][i] * by[u], at);
-                                }
-                                by[u] = 1.0f;
-                            }
+                        for (int h = 0; h < HS; ++h) {
+                            by[2 * h] = shape.by(gp[2 * (h0 + h)].ks, to_log2);
+                            by[2 * h + 1] = shape.by(gp[2 * (h0 + h) + 1].ks, to_log2);
+                            shape_scores(shape, s[h], by + 2 * h,
+                                         (float)(row.pos - (t0 + 32 * (h0 + h) + 4 * g)));
                         }
                     }
                     if (!seen) {
@@ -1082,6 +1104,8 @@ __device__ inline float chunk_weight(float pm, float pl, float at) {
     if (pl != pl) return pl;
     return pl == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(pm - at);
 }
+
+#include "q8_attn_mid.h"
 
 // Joins the chunks of one output row: first their weights, then the weighted
 // sum, a thread for four dims and the chunks dealt to the workgroup's lanes.
@@ -1186,6 +1210,7 @@ __global__ __launch_bounds__(256) void attn_q8_join_few_kernel(AttnQ8 a, int row
 // empty.
 struct Cut {
     bool many;  // the kernel for many rows
+    bool mid;   // the one for drafts
     int tiles, splits, chunk;
     int span;    // keys of one row tile at most, from an aligned start
     int pieces;  // few rows: chunks in all to aim at, 0 for the chunk as it is
@@ -1204,7 +1229,16 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
     // 4000] 100 / 102, 116 / 105, 136 / 107.  (float32 would stay with the
     // first up to about 64 rows: [64 x 4000], 33 rows, 112 / 149.)
     r.many = rows > 32;
-    const int height = r.many ? 32 * kWaves : 16, step = r.many ? 64 : 32 * kWaves;
+    // With rules, the kernel for drafts between them.  This one / the others in
+    // us, bfloat16, 12 over 4 heads of 128, drafts of one size: [16 x 12000
+    // keys] 24 rows 47 / 83, 48 rows 67 / 79, 96 rows 108 / 95, 192 rows 178 /
+    // 160, 258 rows 236 / 233; [64 x 4000] 56 / 100, 94 / 108, 148 / 126, 248 /
+    // 217; [16 x 500 to 24000] 48 rows 121 / 117, 96 rows 146 / 156, 192 rows
+    // 212 / 284, drafts of 99 to 192 rows 188 / 225; heads of 256, [16 x
+    // 12000], 96 rows 139 / 168, 192 rows 229 / 261.
+    r.mid = rules && rows > 16 && rows <= 192;
+    const int height = r.mid ? 32 : r.many ? 32 * kWaves : 16;
+    const int step = r.many && !r.mid ? 64 : 32 * kWaves;
     r.tiles = (int)((rows + height - 1) / height);
     r.span = max_len;
     if (window > 0)
@@ -1212,11 +1246,17 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
             r.span, (long long)window + height / group + 65 + (prefix > 0 ? prefix + 126LL : 0));
     const long long pairs = (long long)seqs * heads * r.tiles;
     r.pieces = 0;
-    if (r.many && rules && r.tiles <= 4) {
-        // Drafts over long sequences
+    if (r.mid) {
+        const int resident = 256 * mid_residency(dim);
+        r.chunk = std::max(round_up_to((r.span * pairs + resident - 1) / resident, step), step);
+        if (seqs <= 64) r.pieces = resident;
+    } else if (r.many && rules && r.tiles <= 4) {
+        // Drafts over long sequences: cut so that two workgroups a CU have
+        // work to the end ([16 x 500 to 24000 keys], drafts of 99 to 192 rows:
+        // 315 us cut by the longest sequence alone, 225 so).
         const int resident = 512;
         r.chunk = std::max(round_up_to((r.span * pairs + resident - 1) / resident, step), 256);
-        if (seqs > 1 && seqs <= 1024) r.pieces = resident;
+        if (seqs <= 64) r.pieces = resident;
     } else if (r.many) {
         // Split only to give every CU a workgroup, in chunks of 128 keys or
         // more: the joined parts are float32 rows ([4 x 512 rows, 1000 keys,
@@ -1239,6 +1279,12 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
     return r;
 }
 
+// Workgroups of the kernel for drafts: a number for each XCD, the tiles of
+// one sequence, head and chunk on the same.
+inline long long mid_blocks(const Cut& k, int heads, int seqs) {
+    return ((long long)k.splits * heads * seqs + 7) / 8 * 8 * k.tiles;
+}
+
 // Which join: a wave a row wants rows for the CUs ([1 x 2400 keys, 12 heads]
 // takes 15.6 us with it, 13.5 with a workgroup a row).
 inline bool join_by_waves(int splits, long long rows) { return splits <= 64 && rows >= 2048; }
@@ -1255,7 +1301,17 @@ hipError_t run(const AttnQ8& a, R x, const CacheQ8& c, const Ragged& r, float* p
         x.pieces = k.pieces;
         x.span = k.span;
     }
-    if (k.many)
+    bool mid = false;
+    if constexpr (kRules<R>) {
+        mid = k.mid;
+        if (mid)
+            hipLaunchKernelGGL((attn_q8_mid_kernel<T, D>),
+                               dim3((unsigned)mid_blocks(k, c.heads, r.seqs)), dim3(64 * kWaves),
+                               0, stream, a, c, r, x, k.splits, k.chunk, k.tiles, part);
+    }
+    if (mid)
+        ;
+    else if (k.many)
         hipLaunchKernelGGL((attn_q8_many_kernel<T, D, R>),
                            dim3((unsigned)blocks),
                            dim3(64 * kWaves), 0, stream, a, c, r, x, k.splits, k.chunk, k.tiles, part);

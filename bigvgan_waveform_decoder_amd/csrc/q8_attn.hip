@@ -14,7 +14,8 @@ long long attn_q8_workgroups(int seqs, int total, int max_rows, int max_len, int
                              int heads, int dim, int elem, int window, int prefix,
                              bool rules) {
     const Cut k = cut(seqs, max_rows, max_len, q_heads, heads, dim, elem, window, prefix, rules);
-    const long long blocks = (long long)k.tiles * k.splits * heads * seqs;
+    const long long blocks =
+        k.mid ? mid_blocks(k, heads, seqs) : (long long)k.tiles * k.splits * heads * seqs;
     const long long rows = (long long)total * q_heads;
     if (k.splits == 1) return blocks;
     return std::max(blocks, join_by_waves(k.splits, rows) ? rows / 4 + 1 : 2 * rows);
