@@ -33,7 +33,8 @@ def _near(got, want, size, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dim,rot", [(64, 64), (64, 26), (128, 128), (128, 50), (128, 0), (256, 256),
-                                     (80, 80), (96, 24), (2, 2), (10, 6), (512, 512), (130, 66)])
+                                     (80, 80), (96, 24), (2, 2), (10, 6), (512, 512), (130, 66),
+                                     (64, 50), (64, 4), (64, 60), (512, 50), (100, 100)])
 def test_turned_heads(dim, rot, interleaved, dtype):
     """Lengths from none to many, heads beside each other in one product's
     rows, with and without the norm, in place and not."""
@@ -207,7 +208,8 @@ WRITES = [  # new tokens, lengths afterwards, page
 @pytest.mark.parametrize("case", range(len(WRITES)))
 @pytest.mark.parametrize("heads,dim,rot,interleaved", [(1, 64, 64, True), (3, 128, 128, False),
                                                        (2, 256, 90, False), (2, 64, 30, True),
-                                                       (2, 128, 64, False)])
+                                                       (2, 128, 64, False), (1, 64, 60, False),
+                                                       (1, 64, 50, False), (2, 256, 4, False)])
 def test_turned_cache_write(case, heads, dim, rot, interleaved, dtype):
     new, lens, page = WRITES[case]
     announce(f"kv_write_rope_q8 {new} {lens} page {page} heads {heads} dim {dim} rot {rot} {dtype}")
