@@ -853,6 +853,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
         }
         Group to = next;
         to.ks = to.on ? to.ks : 0.0f;
+        if constexpr (kRules<R>)
+            if (!finite(to.ks)) to.ks = nan();  // stays with the score whatever the cap
         to.vs = to.on ? to.vs : 0.0f;
         to.on |= finite(to.vs) ? 0 : 2;
         to.lg_vs = finite(to.vs) ? __builtin_amdgcn_logf(to.vs) : neg_inf();
@@ -999,8 +1001,6 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
                     if constexpr (kRules<R>) {
 #pragma unroll
                         for (int h = 0; h < HS; ++h) {
-                            by[2 * h] = shape.by(gp[2 * (h0 + h)].ks, to_log2);
-                            by[2 * h + 1] = shape.by(gp[2 * (h0 + h) + 1].ks, to_log2);
                             shape_scores(shape, s[h], by + 2 * h,
                                          (float)(row.pos - (t0 + 32 * (h0 + h) + 4 * g)));
                         }

@@ -14,6 +14,14 @@ rows and weights; the residual stream and what lies between two operators is
 bfloat16.  A step of one frame a stream and a prompt of many run the same
 calls.
 
+By its Config a network adds positions to the embedded frames, or turns
+queries and keys by them (rot), norms each head (head_norm), caps its scores
+(cap), sees a window of the last frames, and of its prompt all (sees_prompt).
+Drafted frames are checked at once, as a tree:
+
+    after = gen.check(drafts, parents)     # the next frame after each draft
+    gen.keep(paths)                        # goes on from those that are right
+
 ``python -m bigvgan_waveform_decoder_amd.latents`` generates latents, decodes
 them and prints the times.
 """
@@ -39,12 +47,22 @@ class Config:
     hidden: int = 6144
     page: int = 64
     eps: float = 1e-6
+    rot: int = 0                # dims of a head that positions turn; 0: they are added to the frames
+    theta: float = 10000.0
+    head_norm: bool = False     # RMS norm of each query and key head
+    cap: float = 0.0            # scores become cap * tanh(score / cap); 0: as they are
+    window: int = 0             # frames in view; 0: all
+    sees_prompt: bool = False   # a prompt sees itself whole, and stays in view of the window
 
     def __post_init__(self):
         if self.heads % self.kv_heads:
             raise ValueError(f"{self.heads} query heads over {self.kv_heads} cache heads")
         if min(self.c_latent, self.width, self.layers, self.hidden) < 1:
             raise ValueError("sizes must be at least 1")
+        if self.rot % 2 or not 0 <= self.rot <= self.dim:
+            raise ValueError(f"{self.rot} of {self.dim} dims cannot be turned in pairs")
+        if self.window < 0:
+            raise ValueError("a window is not negative")
 
     @property
     def qkv(self) -> int:
@@ -70,6 +88,9 @@ def random_weights(cfg: Config, seed: int = 0, device="cuda") -> Dict[str, torch
         w[f"{i}.o"] = product(cfg.width, cfg.heads * cfg.dim, 0.5)
         w[f"{i}.up"] = product(cfg.hidden, cfg.width)
         w[f"{i}.down"] = product(cfg.width, cfg.hidden, 0.5)
+        if cfg.head_norm:
+            for name in ("q_norm", "k_norm"):
+                w[f"{i}.{name}"] = 1 + 0.1 * torch.randn(cfg.dim, generator=g, device=device)
     return w
 
 
@@ -101,23 +122,56 @@ class LatentGenerator:
         self.table = torch.arange(streams * pages, dtype=torch.int32, device=dev).view(streams, pages)
         self.lens = torch.zeros(streams, dtype=torch.int32, device=dev)
         self.one_each = torch.arange(streams + 1, dtype=torch.int32, device=dev)
-        self.longest = 0
+        self.counts = [0] * streams  # what lens holds, on the host
         self.empty = True
+        self.rope = avae.Rope.of(cfg.rot, theta=cfg.theta, device=dev) if cfg.rot else None
+        self.prompt = torch.zeros(streams, dtype=torch.int32, device=dev)
+        self.longest_prompt = 0
+        self.drafts = None  # what keep() needs of the last check(): parents, keys and values a layer
+
+    @property
+    def longest(self) -> int:
+        return max(self.counts)
 
     def _linear(self, q, scale, name, **kw):
         w, w_scale = self.w[name]
         return avae.linear_q8(q, scale, w, w_scale, **kw)
 
-    def _forward(self, frames, cu, most: int):
-        """frames [rows, c_latent] float32, the streams' last ones as cu says
-        (self.lens counts them already) -> [rows, c_latent]."""
+    def _attend(self, q, cache, cu, lens, most: int, longest: int, tree):
+        cfg = self.cfg
+        args = (q, cache, self.table, cu, lens)
+        if tree is not None:
+            return avae.attn_tree_q8(*args, tree, max_q=most, max_len=longest, cap=cfg.cap)
+        if not cfg.cap and not cfg.sees_prompt:
+            return avae.attn_q8(*args, max_q=most, max_len=longest, window=cfg.window)
+        return avae.attn_rules_q8(*args, max_q=most, max_len=longest, window=cfg.window, cap=cfg.cap,
+                                  prefix=self.prompt if cfg.sees_prompt else None,
+                                  max_prefix=self.longest_prompt)
+
+    def _write(self, i: int, k, v, cu, lens, most: int, positions=None):
+        """Keys and values of layer i into its cache."""
+        if self.rope is None and not self.cfg.head_norm:
+            avae.kv_write_q8(self.caches[i], k, v, self.table, cu, lens, max_new=most)
+        else:
+            avae.kv_write_rope_q8(self.caches[i], k, v, self.table, cu, lens, self.rope,
+                                  k_weight=self.w.get(f"{i}.k_norm"), eps=self.cfg.eps,
+                                  positions=positions, max_new=most)
+
+    def _forward(self, frames, cu, lens, most: int, longest: int, tree=None, positions=None):
+        """frames [rows, c_latent] float32, the streams' last ones as cu and
+        lens say (at their places, or drafts at `positions` that see each other
+        by `tree`) -> [rows, c_latent], and keys and values a layer."""
         cfg, bf16 = self.cfg, torch.bfloat16
         rows = frames.shape[0]
-        stream = torch.searchsorted(cu[1:].long(), torch.arange(rows, device=frames.device), right=True)
-        at = self.lens.long()[stream] - cu.long()[stream + 1] + torch.arange(rows, device=frames.device)
+        at = positions
+        if at is None:
+            row = torch.arange(rows, device=frames.device)
+            stream = torch.searchsorted(cu[1:].long(), row, right=True)
+            at = lens.long()[stream] - cu.long()[stream + 1] + row
         # the embedded frame and its position start the residual stream
         delta = self._linear(*avae.quant_q8(frames), "in", dtype=bf16)
-        h = self.pos[at]
+        h = self.pos[at.long()] if not cfg.rot else torch.zeros_like(delta)
+        kept = []
         n_q, n_kv = cfg.heads * cfg.dim, cfg.kv_heads * cfg.dim
         for i, cache in enumerate(self.caches):
             q8, s, h = avae.rms_norm_q8(delta, self.w[f"{i}.norm1"], cfg.eps, residual=h)
@@ -125,14 +179,19 @@ class LatentGenerator:
             q = qkv[:, :n_q].unflatten(1, (cfg.heads, cfg.dim))
             k = qkv[:, n_q:n_q + n_kv].unflatten(1, (cfg.kv_heads, cfg.dim))
             v = qkv[:, n_q + n_kv:].unflatten(1, (cfg.kv_heads, cfg.dim))
-            avae.kv_write_q8(cache, k, v, self.table, cu, self.lens, max_new=most)
-            a = avae.attn_q8(q, cache, self.table, cu, self.lens, max_q=most, max_len=self.longest)
+            if self.rope is not None or cfg.head_norm:
+                q, _ = avae.qk_norm_rope(q, None, self.rope, self.w.get(f"{i}.q_norm"), eps=cfg.eps,
+                                         positions=positions, cu=cu, lens=lens, max_rows=most,
+                                         inplace=True)
+            self._write(i, k, v, cu, lens, most, positions)
+            kept.append((k, v))
+            a = self._attend(q, cache, cu, lens, most, longest, tree)
             delta = self._linear(*avae.quant_q8(a.flatten(1)), f"{i}.o", dtype=bf16)
             q8, s, h = avae.rms_norm_q8(delta, self.w[f"{i}.norm2"], cfg.eps, residual=h)
             u = self._linear(q8, s, f"{i}.up", act="silu", dtype=bf16)
             delta = self._linear(*avae.quant_q8(u), f"{i}.down", dtype=bf16)
         q8, s, _ = avae.rms_norm_q8(delta, self.w["norm"], cfg.eps, residual=h)
-        return self._linear(q8, s, "out", bias=self.w["out_bias"])
+        return self._linear(q8, s, "out", bias=self.w["out_bias"]), kept
 
     def prefill(self, prompts: Sequence[torch.Tensor]) -> torch.Tensor:
         """One prompt [n, c_latent] a stream (n >= 1) -> the next frame of
@@ -148,8 +207,11 @@ class LatentGenerator:
         dev = self.lens.device
         cu = torch.tensor([0] + counts, dtype=torch.int32, device=dev).cumsum(0).int()
         self.lens.copy_(torch.tensor(counts, dtype=torch.int32))
-        self.longest, self.empty = max(counts), False
-        y = self._forward(torch.cat([p.float() for p in prompts]).to(dev).contiguous(), cu, max(counts))
+        self.counts, self.empty = counts, False
+        self.prompt.copy_(self.lens)
+        self.longest_prompt = self.longest
+        y, _ = self._forward(torch.cat([p.float() for p in prompts]).to(dev).contiguous(), cu, self.lens,
+                             max(counts), self.longest)
         return y[cu[1:].long() - 1]
 
     def step(self, frames: torch.Tensor) -> torch.Tensor:
@@ -161,8 +223,68 @@ class LatentGenerator:
         if self.longest >= self.max_frames:
             raise ValueError(f"{self.max_frames} frames are written")
         self.lens += 1
-        self.longest += 1
-        return self._forward(frames.float().contiguous(), self.one_each, 1)
+        self.counts = [n + 1 for n in self.counts]
+        self.drafts = None
+        return self._forward(frames.float().contiguous(), self.one_each, self.lens, 1, self.longest)[0]
+
+    def check(self, drafts: Sequence[torch.Tensor], parents: Sequence[Sequence[int]]) -> List[torch.Tensor]:
+        """Drafted frames [n, c_latent] of each stream (n may be 0), draft i
+        following draft parents[i] < i of its stream or, with -1, the stream's
+        last frame -> the next frame after each draft, [n, c_latent] a stream.
+        The streams stay where they are: keep() goes on."""
+        cfg = self.cfg
+        if self.empty:
+            raise ValueError("a prompt comes first")
+        if cfg.window:
+            raise ValueError("drafts are checked without a window")
+        if len(drafts) != self.streams or any(
+                d.dim() != 2 or d.shape[1] != cfg.c_latent or d.shape[0] != len(p)
+                for d, p in zip(drafts, parents)) or len(parents) != self.streams:
+            raise ValueError(f"expected {self.streams} drafts [n, {cfg.c_latent}], a parent each")
+        if any(not -1 <= p < i for up in parents for i, p in enumerate(up)):
+            raise ValueError("a draft's parent comes before it")
+        new = [d.shape[0] for d in drafts]
+        most, longest = max(new), max(a + b for a, b in zip(self.counts, new))
+        if longest > self.max_frames:
+            raise ValueError(f"drafts up to frame {longest}: at most {self.max_frames}")
+        parents, kept = [list(p) for p in parents], []
+        if most == 0:
+            y = torch.cat([d.float() for d in drafts])
+        else:
+            dev = self.lens.device
+            cu = torch.tensor([0] + new, dtype=torch.int32).cumsum(0).int().to(dev)
+            lens = self.lens + (cu[1:] - cu[:-1])
+            up = torch.tensor([p for u in parents for p in u], dtype=torch.int32, device=dev)
+            tree, positions = avae.tree_mask(up, cu, lens, max_rows=most)
+            y, kept = self._forward(torch.cat([d.float() for d in drafts]).to(dev).contiguous(), cu,
+                                    lens, most, longest, tree, positions)
+        self.drafts = (parents, kept)
+        return list(y.split(new))
+
+    def keep(self, paths: Sequence[Sequence[int]]) -> None:
+        """Goes on from the last check(): of each stream's drafts those of its
+        path, from one that follows the stream down, become its frames (none
+        of an empty path)."""
+        if self.drafts is None:
+            raise ValueError("a check comes first")
+        parents, kept = self.drafts
+        if len(paths) != self.streams or any(
+                not 0 <= i < len(up) or up[i] != before
+                for path, up in zip(paths, parents) for before, i in zip([-1, *path], path)):
+            raise ValueError("a path goes down through its stream's drafts, each to one that follows it")
+        self.drafts = None
+        new = [len(p) for p in paths]
+        if max(new) == 0:
+            return
+        dev = self.lens.device
+        cu = torch.tensor([0] + new, dtype=torch.int32).cumsum(0).int().to(dev)
+        starts = [sum(len(u) for u in parents[:b]) for b in range(self.streams)]
+        rows = torch.tensor([s + i for s, p in zip(starts, paths) for i in p], device=dev)
+        self.lens += cu[1:] - cu[:-1]
+        self.counts = [a + b for a, b in zip(self.counts, new)]
+        for i, (k, v) in enumerate(kept):
+            # written anew, one after the other, over what the drafts left
+            self._write(i, k[rows], v[rows], cu, self.lens, max(new))
 
     def generate(self, prompts: Sequence[torch.Tensor], frames: int) -> torch.Tensor:
         """`frames` new frames of each stream after its prompt -> latent
