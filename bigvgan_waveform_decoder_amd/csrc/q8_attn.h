@@ -1107,16 +1107,30 @@ __device__ inline float chunk_weight(float pm, float pl, float at) {
 
 #include "q8_attn_mid.h"
 
+// The output row of a join's i-th: with rules counted in a sequence (blockIdx.y),
+// so that rows of no sequence stay as they were; -1 past the end.
+template <typename R>
+__device__ inline long long joined_row(const AttnQ8& a, const R&, const Ragged& r, long long i) {
+    if constexpr (kRules<R>) {
+        int cu0, n, len;
+        if (!ragged_rows(r, blockIdx.y, cu0, n, len)) return -1;
+        return i < (long long)min(n, r.max_rows) * a.q_heads ? (long long)cu0 * a.q_heads + i : -1;
+    } else {
+        return i < (long long)r.total * a.q_heads ? i : -1;
+    }
+}
+
 // Joins the chunks of one output row: first their weights, then the weighted
 // sum, a thread for four dims and the chunks dealt to the workgroup's lanes.
-template <typename T, int D>
-__global__ __launch_bounds__(512) void attn_q8_join_kernel(AttnQ8 a, int splits,
+template <typename T, int D, typename R>
+__global__ __launch_bounds__(512) void attn_q8_join_kernel(AttnQ8 a, R x, Ragged r, int splits,
                                                            const float* __restrict__ part) {
     constexpr int COLS = D / 4, LANES = 512 / COLS;
     __shared__ float s_by[kMaxSplits];
     __shared__ f4 s_out[512];
     __shared__ float s_m[8], s_l[8];
-    const long long row = blockIdx.x;
+    const long long row = joined_row(a, x, r, blockIdx.x);
+    if (row < 0) return;
     const float* pr = part + row * splits * (D + 4);
     float m = neg_inf();
     for (int s = threadIdx.x; s < splits; s += 512) {
@@ -1166,13 +1180,13 @@ __global__ __launch_bounds__(512) void attn_q8_join_kernel(AttnQ8 a, int splits,
 
 // The same for up to 64 chunks, a wave a row: a lane for a chunk's weight,
 // then for four dims of some of them.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void attn_q8_join_few_kernel(AttnQ8 a, int rows, int splits,
+template <typename T, int D, typename R>
+__global__ __launch_bounds__(256) void attn_q8_join_few_kernel(AttnQ8 a, R x, Ragged r, int splits,
                                                                const float* __restrict__ part) {
     constexpr int COLS = D / 4, LANES = 64 / COLS;
     const int lane = threadIdx.x & 63;
-    const long long row = blockIdx.x * 4LL + wave_id();
-    if (row >= rows) return;
+    const long long row = joined_row(a, x, r, blockIdx.x * 4LL + wave_id());
+    if (row < 0) return;
     const float* pr = part + row * splits * (D + 4);
     float m = neg_inf(), l = 0.0f;
     if (lane < splits) {
@@ -1322,13 +1336,16 @@ hipError_t run(const AttnQ8& a, R x, const CacheQ8& c, const Ragged& r, float* p
                            k.pieces, c.heads * k.tiles, part);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && k.splits > 1) {
-        const int rows = r.total * a.q_heads;
+        const long long rows = (long long)r.total * a.q_heads;
+        const long long each = kRules<R> ? (long long)r.max_rows * a.q_heads : rows;
+        const unsigned seqs = kRules<R> ? r.seqs : 1;
         if (join_by_waves(k.splits, rows))
-            hipLaunchKernelGGL((attn_q8_join_few_kernel<T, D>), dim3((unsigned)(rows + 3LL) / 4),
-                               dim3(256), 0, stream, a, rows, k.splits, part);
+            hipLaunchKernelGGL((attn_q8_join_few_kernel<T, D, R>),
+                               dim3((unsigned)((each + 3) / 4), seqs), dim3(256), 0, stream, a, x,
+                               r, k.splits, part);
         else
-            hipLaunchKernelGGL((attn_q8_join_kernel<T, D>), dim3((unsigned)rows), dim3(512), 0,
-                               stream, a, k.splits, part);
+            hipLaunchKernelGGL((attn_q8_join_kernel<T, D, R>), dim3((unsigned)each, seqs),
+                               dim3(512), 0, stream, a, x, r, k.splits, part);
         e = hipGetLastError();
     }
     return e;

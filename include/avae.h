@@ -758,7 +758,8 @@ int avae_kv_write_rope_q8(const void* k, long long k_tok, long long k_head, cons
  *     only if its bit is set.  Goes with causal attention and first, not
  *     with window, slopes or prefix.  At most AVAE_TREE_MAX_WORDS words.
  * first hides keys from all of this.  A row before its sequence's first token
- * (more rows than tokens) sees nothing.
+ * (more rows than tokens) sees nothing.  Rows of no sequence stay as they
+ * were.
  * Errors: as avae_attn_q8; EINVAL (cap not 0 and not in 1e-30 .. 1e30, rules
  *   that do not go together), ESHAPE (a mask too small for max_rows).
  *
