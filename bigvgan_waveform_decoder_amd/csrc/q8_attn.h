@@ -305,8 +305,15 @@ constexpr int kWaves = 4;
 
 // Waves a SIMD of the kernel for few rows: as many as its registers allow
 // without spills, for the bytes in flight.
-constexpr int few_residency(int dim, int elem) {
+constexpr int few_residency(int dim, int elem, int waves = kWaves) {
+    if (waves > kWaves) return waves / 4;  // one workgroup a CU
     return dim > 128 ? 2 : elem == 4 && dim == 128 ? 3 : 4;
+}
+
+// Waves of its workgroups where they take all the keys of their rows: what
+// fits the registers.
+constexpr int wide_waves(int dim, int elem) {
+    return dim > 128 || (elem == 4 && dim == 128) ? 8 : 16;
 }
 
 // Few query rows: one tile of 16 rows a workgroup, the keys of one chunk
@@ -323,16 +330,16 @@ constexpr int few_residency(int dim, int elem) {
 //
 // With rules the keys in view may lie in two runs, [first, pre) and the
 // window's; they are counted through, u, and cut as one.
-template <typename T, int D, typename R>
-__global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn_q8_few_kernel(AttnQ8 a, CacheQ8 c, Ragged r, R x,
+template <typename T, int D, typename R, int W>
+__global__ __launch_bounds__(64 * W, few_residency(D, sizeof(T), W)) void attn_q8_few_kernel(AttnQ8 a, CacheQ8 c, Ragged r, R x,
                                                                   int splits, int chunk, int span,
                                                                   int pieces, int pairs,
                                                                   float* part) {
     constexpr bool kSplit = Query<T, D>::kSplit;
     constexpr int DT = D / 16;  // output tiles
     constexpr int LD = D + 4;
-    __shared__ float s_out[kWaves * 16 * LD];
-    __shared__ float s_m[kWaves * 16], s_l[kWaves * 16];
+    __shared__ float s_out[W * 16 * LD];
+    __shared__ float s_m[W * 16], s_l[W * 16];
     const int lane = threadIdx.x & 63, wave = wave_id(), n16 = lane & 15, g = lane >> 4;
     // Sequences, heads and tiles side by side, chunks after one another:
     // workgroups go to the XCDs in turn, and the last chunks may be empty.
@@ -351,7 +358,8 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
         for (int o = 32; o > 0; o >>= 1) keys += __shfl_xor(keys, o);
         const long long even = (keys * pairs + pieces - 1) / pieces;
         const int least = (span + splits - 1) / splits;
-        chunk = (min(chunk, max((int)min(even, (long long)chunk), least)) + 127) & ~127;
+        chunk = (min(chunk, max((int)min(even, (long long)chunk), least)) + 32 * W - 1) &
+                ~(32 * W - 1);
     }
     const Row row = row_of(a, c, x, b, head, cu0, n, len, tile * 16 + n16);
     int any_lo, any_hi, all_lo, all_hi;
@@ -415,7 +423,7 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
     // v_run: the largest value scale so far, the accumulated values' unit; at
     // least float32's smallest normal number, which has a reciprocal
     float m = neg_inf(), l = 0.0f, v_run = 0x1p-126f;
-    for (int u0 = t_lo + 32 * wave; u0 < t_hi; u0 += 32 * kWaves) {
+    for (int u0 = t_lo + 32 * wave; u0 < t_hi; u0 += 32 * W) {
         const int t0 = key_at(u0);
         f4 s[2];
         float vs[2];
@@ -442,7 +450,7 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
             ks[h] = c.k_scale[at];
             vs[h] = c.v_scale[at];
         }
-        look_up(key_at(u0 + 32 * kWaves));
+        look_up(key_at(u0 + 32 * W));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             f4 sum = {};
@@ -572,15 +580,15 @@ __global__ __launch_bounds__(64 * kWaves, few_residency(D, sizeof(T))) void attn
     }
     __syncthreads();
     // each thread joins four dims of a row
-    for (int e = threadIdx.x; e < 16 * (D / 4); e += 64 * kWaves) {
+    for (int e = threadIdx.x; e < 16 * (D / 4); e += 64 * W) {
         const int i = e / (D / 4), d = e % (D / 4) * 4;
         const Row to = row_of(a, c, x, b, head, cu0, n, len, tile * 16 + i);
         if (!to.live) break;  // rows come in order
         float top = neg_inf(), sum = 0.0f;
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_m[w * 16 + i]);
+        for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w * 16 + i]);
         const float at = top == neg_inf() ? 0.0f : top;
         f4 o = {};
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float by = __builtin_amdgcn_exp2f(s_m[w * 16 + i] - at);
             sum += by * s_l[w * 16 + i];
             o += by * *reinterpret_cast<const f4*>(s_out + (w * 16 + i) * LD + d);
@@ -1225,6 +1233,7 @@ __global__ __launch_bounds__(256) void attn_q8_join_few_kernel(AttnQ8 a, R x, Ra
 struct Cut {
     bool many;  // the kernel for many rows
     bool mid;   // the one for drafts
+    bool wide;  // the one for few rows (drafts), with wide_waves (mid_wide_waves)
     int tiles, splits, chunk;
     int span;    // keys of one row tile at most, from an aligned start
     int pieces;  // few rows: chunks in all to aim at, 0 for the chunk as it is
@@ -1260,6 +1269,20 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
             r.span, (long long)window + height / group + 65 + (prefix > 0 ? prefix + 126LL : 0));
     const long long pairs = (long long)seqs * heads * r.tiles;
     r.pieces = 0;
+    // With rules and few rows, larger workgroups that take all keys of theirs
+    // where that is two steps, or where there is nearly one for every CU: no
+    // second launch joins chunks.  Whole / split, us for a call, bfloat16, 12
+    // over 4 heads of 128: [1 x 300 keys] 15.0 / 19.5, [1 x 700] 15.4 / 19.3,
+    // [1 x 1500] 21.0 / 19.4, [32 x 1500] 22.3 / 22.0, [64 x 1500] 25.1 / 30.1,
+    // [64 x 6000] 78.7 / 86.3.
+    const int wide = r.mid ? mid_wide_waves(dim) : wide_waves(dim, elem);
+    r.wide = rules && (r.mid || !r.many) && pairs <= 256 && r.span > step &&
+             (r.span <= 64 * wide || (!r.mid && pairs >= 192));
+    if (r.wide) {
+        r.chunk = round_up_to(r.span, 32 * wide);
+        r.splits = 1;
+        return r;
+    }
     if (r.mid) {
         const int resident = 256 * mid_residency(dim);
         r.chunk = std::max(round_up_to((r.span * pairs + resident - 1) / resident, step), step);
@@ -1315,22 +1338,30 @@ hipError_t run(const AttnQ8& a, R x, const CacheQ8& c, const Ragged& r, float* p
         x.pieces = k.pieces;
         x.span = k.span;
     }
-    bool mid = false;
+    bool launched = false;
     if constexpr (kRules<R>) {
-        mid = k.mid;
-        if (mid)
-            hipLaunchKernelGGL((attn_q8_mid_kernel<T, D>),
-                               dim3((unsigned)mid_blocks(k, c.heads, r.seqs)), dim3(64 * kWaves),
-                               0, stream, a, c, r, x, k.splits, k.chunk, k.tiles, part);
+        launched = k.mid || k.wide;
+        const dim3 grid((unsigned)(k.mid ? mid_blocks(k, c.heads, r.seqs) : blocks));
+        constexpr int W = wide_waves(D, sizeof(T)), MW = mid_wide_waves(D);
+        if (k.mid && k.wide)
+            hipLaunchKernelGGL((attn_q8_mid_kernel<T, D, MW>), grid, dim3(64 * MW), 0, stream, a, c,
+                               r, x, k.splits, k.chunk, k.tiles, part);
+        else if (k.mid)
+            hipLaunchKernelGGL((attn_q8_mid_kernel<T, D, kWaves>), grid, dim3(64 * kWaves), 0,
+                               stream, a, c, r, x, k.splits, k.chunk, k.tiles, part);
+        else if (k.wide)
+            hipLaunchKernelGGL((attn_q8_few_kernel<T, D, R, W>), grid, dim3(64 * W), 0, stream, a,
+                               c, r, x, k.splits, k.chunk, k.span, k.pieces, c.heads * k.tiles,
+                               part);
     }
-    if (mid)
+    if (launched)
         ;
     else if (k.many)
         hipLaunchKernelGGL((attn_q8_many_kernel<T, D, R>),
                            dim3((unsigned)blocks),
                            dim3(64 * kWaves), 0, stream, a, c, r, x, k.splits, k.chunk, k.tiles, part);
     else
-        hipLaunchKernelGGL((attn_q8_few_kernel<T, D, R>),
+        hipLaunchKernelGGL((attn_q8_few_kernel<T, D, R, kWaves>),
                            dim3((unsigned)blocks),
                            dim3(64 * kWaves), 0, stream, a, c, r, x, k.splits, k.chunk, k.span,
                            k.pieces, c.heads * k.tiles, part);

@@ -16,6 +16,9 @@
 
 // Waves a SIMD of the kernel below.
 constexpr int mid_residency(int dim) { return dim > 128 ? 1 : 2; }
+// Waves of its workgroups where they take all the keys of their rows: what
+// fits in LDS.
+constexpr int mid_wide_waves(int dim) { return dim > 128 ? 4 : 8; }
 
 template <int N>
 __device__ inline Words<(N + 3) / 4> load_bytes(const int8_t* p) {  // N bytes, N-byte aligned
@@ -28,15 +31,15 @@ __device__ inline Words<(N + 3) / 4> load_bytes(const int8_t* p) {  // N bytes, 
     }
 }
 
-template <typename T, int D>
-__global__ __launch_bounds__(64 * kWaves, mid_residency(D)) void attn_q8_mid_kernel(
+template <typename T, int D, int W>
+__global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
     AttnQ8 a, CacheQ8 c, Ragged r, AttnRules x, int splits, int chunk, int tiles, float* part) {
     constexpr bool kSplit = sizeof(T) == 4;
     constexpr int KC = D / 16;  // key operands of 16 dims
     constexpr int DT = D / 32;  // output tiles; a lane's values of one key, too
     constexpr int LD = D + 4;
-    __shared__ __align__(16) float s_out[kWaves * 32 * LD];
-    __shared__ float s_m[kWaves * 32], s_l[kWaves * 32];
+    __shared__ __align__(16) float s_out[W * 32 * LD];
+    __shared__ float s_m[W * 32], s_l[W * 32];
     const int lane = threadIdx.x & 63, wave = wave_id(), n32 = lane & 31, g = lane >> 5;
     const int pairs = r.seqs * c.heads, tile = (blockIdx.x >> 3) % tiles;
     const long long unit = (long long)((blockIdx.x >> 3) / tiles) * 8 + (blockIdx.x & 7);
@@ -47,7 +50,7 @@ __global__ __launch_bounds__(64 * kWaves, mid_residency(D)) void attn_q8_mid_ker
     if (!ragged_rows(r, b, cu0, n, len)) return;
     const int group = a.q_heads / c.heads, rows = n * group, r0 = tile * 32;
     if (r0 >= rows) return;
-    if (x.pieces) chunk = best_chunk(x, c, r, lane, group, 32, splits, 32 * kWaves);
+    if (x.pieces) chunk = best_chunk(x, c, r, lane, group, 32, splits, 32 * W);
     const Row row = row_of(a, c, x, b, head, cu0, n, len, r0 + n32);
     const Row row0 = row_of(a, c, x, b, head, cu0, n, len, r0);
     const Row row1 = row_of(a, c, x, b, head, cu0, n, len, min(r0 + 31, rows - 1));
@@ -126,7 +129,7 @@ __global__ __launch_bounds__(64 * kWaves, mid_residency(D)) void attn_q8_mid_ker
     look_up(u_first);
     fetch_keys(u_first);
     fetch_values();
-    look_up(u_first + 32 * kWaves);
+    look_up(u_first + 32 * W);
 
     h8 qh[KC], ql[kSplit ? KC : 1];
     float to_log2;  // not negative: the scale's sign goes into the rows
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(64 * kWaves, mid_residency(D)) void attn_q8_mid_ker
     // largest logarithm of a value scale so far (below every one at first).
     float lg_run = -140.0f;
 
-    for (int u0 = u_first; u0 < u_hi; u0 += 32 * kWaves) {
+    for (int u0 = u_first; u0 < u_hi; u0 += 32 * W) {
         const int t0 = key_at(u0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -181,8 +184,8 @@ __global__ __launch_bounds__(64 * kWaves, mid_residency(D)) void attn_q8_mid_ker
             }
         }
         // (what is asked for past the last step is of no use, and harmless)
-        fetch_keys(u0 + 32 * kWaves);
-        look_up(u0 + 64 * kWaves);
+        fetch_keys(u0 + 32 * W);
+        look_up(u0 + 64 * W);
 
         float by[2] = {shape.by(ks[0], to_log2), shape.by(ks[1], to_log2)};
         shape_scores(shape, s, by, (float)(row.pos - (t0 + 4 * g)));
@@ -297,27 +300,27 @@ __global__ __launch_bounds__(64 * kWaves, mid_residency(D)) void attn_q8_mid_ker
     const float half = __builtin_amdgcn_exp2f(0.5f * (lg_run - 15.0f));
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        constexpr int W = DT < 4 ? DT : 4;
+        constexpr int N = DT < 4 ? DT : 4;
 #pragma unroll
-        for (int t = 0; t < DT; t += W) {
-            Pack<float, W> o;
+        for (int t = 0; t < DT; t += N) {
+            Pack<float, N> o;
 #pragma unroll
-            for (int e = 0; e < W; ++e) o.v[e] = acc[t + e][i] * half * half;
-            *reinterpret_cast<Pack<float, W>*>(s_out + (wave * 32 + n32) * LD +
+            for (int e = 0; e < N; ++e) o.v[e] = acc[t + e][i] * half * half;
+            *reinterpret_cast<Pack<float, N>*>(s_out + (wave * 32 + n32) * LD +
                                                DT * (8 * (i >> 2) + 4 * g + (i & 3)) + t) = o;
         }
     }
     __syncthreads();
     // each thread joins four dims of a row
-    for (int e = threadIdx.x; e < 32 * (D / 4); e += 64 * kWaves) {
+    for (int e = threadIdx.x; e < 32 * (D / 4); e += 64 * W) {
         const int i = e / (D / 4), d = e % (D / 4) * 4;
         const Row to = row_of(a, c, x, b, head, cu0, n, len, r0 + i);
         if (!to.live) break;  // rows come in order
         float top = neg_inf(), sum = 0.0f;
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, s_m[w * 32 + i]);
+        for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w * 32 + i]);
         const float base_m = top == neg_inf() ? 0.0f : top;
         f4 o = {};
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float by = chunk_weight(s_m[w * 32 + i], s_l[w * 32 + i], base_m);
             if (by == 0.0f) continue;
             sum += by * s_l[w * 32 + i];
