@@ -951,10 +951,9 @@ class _Env:
         """The raw stream to launch on: the current one of the tensor's device."""
         return self.raw_stream(t.get_device())
 
-    def launch(self, t, f, *args):
-        """f(*args, stream) on the current stream of the tensor's device,
+    def launch(self, dev, f, *args):
+        """f(*args, stream) on the current stream of device number `dev`,
         which is made the current device meanwhile."""
-        dev = t.get_device()
         if dev == self.device():
             rc = f(*args, self.raw_stream(dev))
         else:
@@ -1260,19 +1259,66 @@ class Rope:
         return cls(_torch().from_numpy(freq).to(device), interleaved, amp)
 
 
-def _rows_of(E, cu, lens, total: int, max_rows: Optional[int]):
-    """Sequences without a page table."""
-    seqs = lens.shape[0]
-    return avae_ragged(_vec(cu, "cu", seqs + 1, E.int32), _vec(lens, "lens", seqs, E.int32), None,
-                       0, 0, seqs, total,
+# The checks of the calls below: as those above, and that every tensor is on
+# the first one's device.
+
+def _bad_at(t, name: str, dtype, dev: int, expected: str):
+    if t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.get_device()}, the first tensor on {dev}")
+    _bad(t, name, dtype, expected)
+
+
+def _vec_at(t, name: str, n: int, dtype, dev: int):
+    if (t.get_device() != dev or t.dtype is not dtype or t.shape != (n,)
+            or not t.is_contiguous() or dev < 0):
+        _bad_at(t, name, dtype, dev, f"[{n}]")
+    return t.data_ptr()
+
+
+def _heads_at(t, name: str, dtype, total: int, heads: Optional[int], dim: int, dev: int):
+    """Pointer, token and head stride of a [total, heads, dim] tensor."""
+    shape = t.shape
+    if (len(shape) != 3 or shape[0] != total or shape[2] != dim or t.dtype is not dtype
+            or t.get_device() != dev or dev < 0 or (heads is not None and shape[1] != heads)):
+        _bad_at(t, name, dtype, dev, f"[{total}, {heads or 'heads'}, {dim}]")
+    tok, head, one = t.stride()
+    if one != 1:
+        _bad_at(t, name, dtype, dev, f"[{total}, {heads or 'heads'}, {dim}]")
+    return t.data_ptr(), tok, head
+
+
+def _rows_at(E, table, cu, lens, total: int, max_rows: Optional[int], dev: int):
+    """Packed rows of sequences, with their pages or (table None) without."""
+    i32 = E.int32
+    (seqs,) = lens.shape
+    pt, ld, cols = None, 0, 0
+    if table is not None:
+        shape = table.shape
+        if len(shape) != 2 or shape[0] != seqs or table.dtype is not i32 or table.get_device() != dev:
+            _bad_at(table, "table", i32, dev, f"[{seqs}, pages]")
+        cols = shape[1]
+        ld, one = table.stride()
+        if one != 1 and cols > 1:
+            _bad_at(table, "table", i32, dev, f"[{seqs}, pages]")
+        # the stride of a single row says nothing; torch may give any
+        pt, ld = table.data_ptr(), (ld if seqs > 1 else cols)
+    return avae_ragged(_vec_at(cu, "cu", seqs + 1, i32, dev), _vec_at(lens, "lens", seqs, i32, dev), pt,
+                       ld, cols, seqs, total,
                        total if max_rows is None or max_rows > total else max_rows)
 
 
-def _on(dev: int, *tensors):
-    """Refuses tensors of another device than the first one's."""
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on device {t.get_device()} and on device {dev}")
+def _same_device(cache, dev: int):
+    if cache.k.get_device() != dev:
+        raise ValueError(f"the cache is on device {cache.k.get_device()}, the first tensor on {dev}")
+
+
+def _freq_at(rope: Optional[Rope], dev: int):
+    if rope is None:
+        return None
+    if rope.freq.get_device() != dev:
+        raise ValueError(f"the frequencies are on device {rope.freq.get_device()}, the first tensor "
+                         f"on {dev}")
+    return rope.ref
 
 
 def qk_norm_rope(q, k, rope: Optional[Rope], q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -1289,33 +1335,37 @@ def qk_norm_rope(q, k, rope: Optional[Rope], q_weight=None, k_weight=None, eps: 
     E = _q8()
     if q.dim() != 3:
         raise ValueError(f"q: expected [tokens, heads, dim], got {tuple(q.shape)}")
-    (total, heads, dim), dtype, dev = q.shape, q.dtype, q.device
+    total, heads, dim = q.shape
+    dtype, dev, f32 = q.dtype, q.get_device(), E.float32
     code = E.code(dtype)
-    pq, q_tok, q_head = _heads(q, "q", None, dim)
-    _on(q.get_device(), k, q_weight, k_weight, positions, cu, lens, rope and rope.freq)
-    q_out = q if inplace else E.heads(total, heads, dim, dtype, dev)
-    qo_tok, qo_head, _ = q_out.stride()
+    pq, q_tok, q_head = _heads_at(q, "q", dtype, total, heads, dim, dev)
+    device = q.device
     pk = pko = k_out = None
     k_heads = k_tok = k_head = ko_tok = ko_head = 0
     if k is not None:
-        if k.dtype != dtype or k.dim() != 3 or k.shape[0] != total:
-            raise ValueError("q and k must have one dtype and as many tokens")
+        pk, k_tok, k_head = _heads_at(k, "k", dtype, total, None, dim, dev)
         k_heads = k.shape[1]
-        pk, k_tok, k_head = _heads(k, "k", None, dim)
-        k_out = k if inplace else E.heads(total, k_heads, dim, dtype, dev)
-        pko = k_out.data_ptr()
-        ko_tok, ko_head, _ = k_out.stride()
+        if inplace:
+            k_out, pko, ko_tok, ko_head = k, pk, k_tok, k_head
+        else:
+            k_out = E.heads(total, k_heads, dim, dtype, device)
+            pko, ko_tok, ko_head = k_out.data_ptr(), k_heads * dim, dim
+    if inplace:
+        q_out, pqo, qo_tok, qo_head = q, pq, q_tok, q_head
+    else:
+        q_out = E.heads(total, heads, dim, dtype, device)
+        pqo, qo_tok, qo_head = q_out.data_ptr(), heads * dim, dim
     if (cu is None) != (lens is None):
         raise ValueError("cu and lens are given together or not at all")
-    rows = None if cu is None else _rows_of(E, cu, lens, total, max_rows)
-    E.launch(q, E.qk, pq, q_tok, q_head, heads,
-             None if q_weight is None else _vec(q_weight, "q_weight", dim, E.float32),
+    rows = None if cu is None else _rows_at(E, None, cu, lens, total, max_rows, dev)
+    E.launch(dev, E.qk, pq, q_tok, q_head, heads,
+             None if q_weight is None else _vec_at(q_weight, "q_weight", dim, f32, dev),
              pk, k_tok, k_head, k_heads,
-             None if k_weight is None else _vec(k_weight, "k_weight", dim, E.float32), dim, code,
-             eps, None if rope is None else rope.ref,
-             None if positions is None else _vec(positions, "positions", total, E.int32),
-             None if rows is None else ctypes.addressof(rows), total, q_out.data_ptr(), qo_tok,
-             qo_head, pko, ko_tok, ko_head)
+             None if k_weight is None else _vec_at(k_weight, "k_weight", dim, f32, dev), dim, code,
+             eps, _freq_at(rope, dev),
+             None if positions is None else _vec_at(positions, "positions", total, E.int32, dev),
+             None if rows is None else ctypes.addressof(rows), total, pqo, qo_tok, qo_head, pko,
+             ko_tok, ko_head)
     return q_out, k_out
 
 
@@ -1329,40 +1379,39 @@ def kv_write_rope_q8(cache: KvCacheQ8, k, v, table, cu, lens, rope: Optional[Rop
             return kv_write_rope_q8(cache, k, v, table, cu, lens, rope, k_weight, eps, positions,
                                     max_new)
     E = _q8()
-    total = k.shape[0]
-    if v.dtype != k.dtype or v.shape[0] != total:
-        raise ValueError("k and v must have one dtype and as many tokens")
-    _on(k.get_device(), cache.k, v, table, cu, lens, rope and rope.freq, k_weight, positions)
-    rows = _ragged(E, table, cu, lens, total, max_new)
-    E.launch(
-        k, E.write_rope, *_heads(k, "k", cache.heads, cache.dim),
-        *_heads(v, "v", cache.heads, cache.dim), E.code(k.dtype),
-        None if k_weight is None else _vec(k_weight, "k_weight", cache.dim, E.float32), eps,
-        None if rope is None else rope.ref,
-        None if positions is None else _vec(positions, "positions", total, E.int32),
-        cache.ref, ctypes.addressof(rows))
+    total, dtype, dev = k.shape[0], k.dtype, k.get_device()
+    heads, dim = cache.heads, cache.dim
+    _same_device(cache, dev)
+    rows = _rows_at(E, table, cu, lens, total, max_new, dev)
+    E.launch(dev, E.write_rope, *_heads_at(k, "k", dtype, total, heads, dim, dev),
+             *_heads_at(v, "v", dtype, total, heads, dim, dev), E.code(dtype),
+             None if k_weight is None else _vec_at(k_weight, "k_weight", dim, E.float32, dev), eps,
+             _freq_at(rope, dev),
+             None if positions is None else _vec_at(positions, "positions", total, E.int32, dev),
+             cache.ref, ctypes.addressof(rows))
 
 
 def _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, causal, window, first, rules,
                 return_lse):
     E = _q8()
-    dim, dtype, dev = cache.dim, q.dtype, q.device
+    dim, dtype, dev = cache.dim, q.dtype, q.get_device()
     code = E.code(dtype)
-    pq, tok, head = _heads(q, "q", None, dim)
-    total, heads, _ = q.shape
-    _on(q.get_device(), cache.k, table, cu, lens, first)
-    rows = _ragged(E, table, cu, lens, total, max_q)
+    total = q.shape[0]
+    pq, tok, head = _heads_at(q, "q", dtype, total, None, dim, dev)
+    heads, device = q.shape[1], q.device
+    _same_device(cache, dev)
+    rows = _rows_at(E, table, cu, lens, total, max_q, dev)
     pr, px = ctypes.addressof(rows), ctypes.addressof(rules)
     if max_len is None:
         max_len = rows.table_cols * cache.page
     if rules.max_prefix < 0:
         rules.max_prefix = max_len
-    out = E.heads(total, heads, dim, dtype, dev)
-    lse = E.mat(total, heads, E.float32, dev) if return_lse else None
+    out = E.heads(total, heads, dim, dtype, device)
+    lse = E.mat(total, heads, E.float32, device) if return_lse else None
     need = E.rules_ws(cache.ref, pr, heads, code, max_len, window, px)
-    ws = E.vec(need, E.uint8, dev) if need else None
-    E.launch(q, E.rules, pq, tok, head, heads, code, cache.ref, pr,
-             None if first is None else _vec(first, "first", rows.seqs, E.int32), max_len,
+    ws = E.vec(need, E.uint8, device) if need else None
+    E.launch(dev, E.rules, pq, tok, head, heads, code, cache.ref, pr,
+             None if first is None else _vec_at(first, "first", rows.seqs, E.int32, dev), max_len,
              dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, px,
              out.data_ptr(), None if lse is None else lse.data_ptr(),
              None if ws is None else ws.data_ptr(), need)
@@ -1385,10 +1434,10 @@ def attn_rules_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = N
     E = _q8()
     if max_prefix is not None and max_prefix < 0:
         raise ValueError(f"max_prefix is not negative, got {max_prefix}")
-    _on(q.get_device(), slopes, prefix)
+    dev = q.get_device()
     rules = avae_attn_rules(
-        cap, None if slopes is None else _vec(slopes, "slopes", q.shape[1], E.float32),
-        None if prefix is None else _vec(prefix, "prefix", lens.shape[0], E.int32),
+        cap, None if slopes is None else _vec_at(slopes, "slopes", q.shape[1], E.float32, dev),
+        None if prefix is None else _vec_at(prefix, "prefix", lens.shape[0], E.int32, dev),
         -1 if max_prefix is None else max_prefix, None, 0, 0)
     return _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, causal, window, first,
                        rules, return_lse)
@@ -1405,14 +1454,13 @@ def tree_mask(parents, cu, lens, max_rows: Optional[int] = None, stream=None):
     E = _q8()
     if parents.dim() != 1:
         raise ValueError(f"parents: expected [tokens], got {tuple(parents.shape)}")
-    total = parents.shape[0]
-    p = _vec(parents, "parents", total, E.int32)
-    _on(parents.get_device(), cu, lens)
-    rows = _rows_of(E, cu, lens, total, max_rows)
+    total, dev, device = parents.shape[0], parents.get_device(), parents.device
+    p = _vec_at(parents, "parents", total, E.int32, dev)
+    rows = _rows_at(E, None, cu, lens, total, max_rows, dev)
     words = (rows.max_rows + 31) // 32
-    mask = E.mat(total, words, E.int32, parents.device)
-    positions = E.vec(total, E.int32, parents.device)
-    E.launch(parents, E.tree, p, ctypes.addressof(rows), words, mask.data_ptr(), words,
+    mask = E.mat(total, words, E.int32, device)
+    positions = E.vec(total, E.int32, device)
+    E.launch(dev, E.tree, p, ctypes.addressof(rows), words, mask.data_ptr(), words,
              positions.data_ptr())
     return mask, positions
 
@@ -1430,7 +1478,8 @@ def attn_tree_q8(q, cache: KvCacheQ8, table, cu, lens, tree, max_q: Optional[int
     E = _q8()
     total, words = q.shape[0], _two_axes(tree, "tree")[1]
     p, ld = _rows(tree, "tree", E.int32, total, words)
-    _on(q.get_device(), tree)
+    if tree.get_device() != q.get_device():
+        _bad_at(tree, "tree", E.int32, q.get_device(), f"[{total}, {words}]")
     rules = avae_attn_rules(cap, None, None, 0, p, ld, words)
     return _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, True, 0, first, rules,
                        return_lse)
