@@ -224,9 +224,13 @@ struct Shape {
           quick(sizeof(T) < 4 && x.cap > 0.0f && x.cap <= 256.0f) {
         if (sloped) slope = x.slopes[r.q_head] * kLog2e;
     }
-    // (a scale that is not finite stays with the score whatever the cap)
+    // (a scale that is not finite stays with the score whatever the cap, and
+    // under one a factor past float32 is held: 0 times an infinity is NaN)
     __device__ float by(float ks, float to_log2) const {
-        return finite(ks) ? ks * to_log2 : nan();
+        return finite(ks) ? held(ks * to_log2) : nan();
+    }
+    __device__ float held(float x) const {
+        return capped ? fminf(fmaxf(x, -3.4e38f), 3.4e38f) : x;
     }
     // The cap,
     // of s = 2 y log2 e, over 2 cap
@@ -414,11 +418,11 @@ __global__ __launch_bounds__(64 * W, few_residency(D, sizeof(T), W)) void attn_q
     look_up(key_at(t_lo + 32 * wave));
     Query<T, D> q;
     q.load(a, row, g);
+    const auto shape = shape_of<T>(x, row);
     float to_log2 = q.back * a.scale * kLog2e;
     if constexpr (kRules<R>)
-        if (x.cap > 0.0f) to_log2 = q.back * (a.scale / x.cap);
+        if (x.cap > 0.0f) to_log2 = shape.held(q.back * shape.held(a.scale / x.cap));
 
-    const auto shape = shape_of<T>(x, row);
     f4 acc[DT] = {};
     // v_run: the largest value scale so far, the accumulated values' unit; at
     // least float32's smallest normal number, which has a reciprocal
@@ -654,7 +658,8 @@ constexpr int kStart = 256;
 __device__ inline int best_chunk(const AttnRules& x, const CacheQ8& c, const Ragged& r, int lane,
                                  int group, int height, int splits, int step) {
     const int least = ((x.span + splits - 1) / splits + step - 1) & ~(step - 1);
-    const int chunk = (least + (int)((long long)least * lane / 16) + step - 1) & ~(step - 1);
+    const int more = (int)min((long long)least * lane / 16, (long long)max(x.span - least, 0));
+    const int chunk = (least + more + step - 1) & ~(step - 1);
     int at, count, length = 0, tiles = 0;
     if (lane < r.seqs && ragged_rows(r, lane, at, count, length))
         tiles = ((count * group - 1) / height + 1) * c.heads;
@@ -681,6 +686,12 @@ __device__ inline int best_chunk(const AttnRules& x, const CacheQ8& c, const Rag
     unsigned cost = (__float_as_uint(done) & ~63u) | (unsigned)lane;
     for (int o = 32; o > 0; o >>= 1) cost = min(cost, (unsigned)__shfl_xor((int)cost, o));
     return __builtin_amdgcn_readlane(chunk, __builtin_amdgcn_readfirstlane((int)(cost & 63u)));
+}
+
+// Where chunk `split` starts (past all keys if it is empty: a row sees fewer
+// than 2^30).
+__device__ inline int chunk_start(int base, int split, int chunk) {
+    return (int)min((long long)base + (long long)split * chunk, 1LL << 30);
 }
 
 // 16 keys of one page: their scales, as the softmax takes them.
@@ -742,7 +753,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
     const int pos0 = len - n + r0 / group;
     const int any_lo = a.window ? max(first, pos0 - a.window + 1) : first, any_hi = row1.hi;
     int base = any_lo < any_hi ? any_lo & ~63 : 0;
-    int t_lo = base + split * chunk;
+    int t_lo = kRules<R> ? chunk_start(base, split, chunk) : base + split * chunk;
     int t_hi = any_lo < any_hi ? min(t_lo + chunk, any_hi) : 0;
     // with a prefix besides the window: keys [first, pre) of all rows, then
     // those from `base` on, counted through
@@ -752,7 +763,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
         if (first < pre) {
             in_pre = ((pre + 63) & ~63) - (first & ~63);
             base = max(base, (pre + 63) & ~63);
-            t_lo = split * chunk;
+            t_lo = chunk_start(0, split, chunk);
             t_hi = min(t_lo + chunk, in_pre + max(any_hi - base, 0));
         }
     }
@@ -771,6 +782,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
     const bool idle = r0 + 32 * wave >= rows;
     const Row row = row_of(a, c, x, b, head, cu0, n, len, r0 + 32 * wave + n32);
 
+    const auto shape = shape_of<T>(x, row);
     h8 qh[KC], ql[kSplit ? KC : 1];
     float to_log2;  // not negative: the scale's sign goes into the rows; with a cap, over it
     {
@@ -786,8 +798,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
         to_log2 = __uint_as_float((unsigned)(127 - 14 + e) << 23) * fabsf(a.scale) * kLog2e;
         if constexpr (kRules<R>)
             if (x.cap > 0.0f)
-                to_log2 = __uint_as_float((unsigned)(127 - 14 + e) << 23) *
-                          (fabsf(a.scale) / x.cap);
+                to_log2 = shape.held(__uint_as_float((unsigned)(127 - 14 + e) << 23) *
+                                     shape.held(fabsf(a.scale) / x.cap));
 #pragma unroll
         for (int j = 0; j < KC; ++j)
 #pragma unroll
@@ -872,7 +884,6 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
         s_group[lane == 0 ? buf : 2 + (lane >> 2)][lane == 0 ? wave : lane & 3] = to;
     };
 
-    const auto shape = shape_of<T>(x, row);
     f16v acc[DT] = {};
     float m = neg_inf(), l = 0.0f;
     // The accumulated values are in units of 2^(lg_run - 15), lg_run the
@@ -1009,6 +1020,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
                     if constexpr (kRules<R>) {
 #pragma unroll
                         for (int h = 0; h < HS; ++h) {
+                            by[2 * h] = shape.held(by[2 * h]);
+                            by[2 * h + 1] = shape.held(by[2 * h + 1]);
                             shape_scores(shape, s[h], by + 2 * h,
                                          (float)(row.pos - (t0 + 32 * (h0 + h) + 4 * g)));
                         }

@@ -61,12 +61,12 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
     const int all_hi = x.tree ? min(row0.hi, len - n) : row0.hi;
     // keys [first, pre) of all rows, then those from `base` on, counted through
     int base = any_lo < any_hi ? any_lo & ~31 : 0, in_pre = 0;
-    int u_lo = base + split * chunk;
+    int u_lo = chunk_start(base, split, chunk);
     int u_hi = any_lo < any_hi ? min(u_lo + chunk, any_hi) : 0;
     if (first < pre) {
         in_pre = ((pre + 31) & ~31) - (first & ~31);
         base = max(base, (pre + 31) & ~31);
-        u_lo = split * chunk;
+        u_lo = chunk_start(0, split, chunk);
         u_hi = min(u_lo + chunk, in_pre + max(any_hi - base, 0));
     }
     auto key_at = [&](int u) {
@@ -131,6 +131,7 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
     fetch_values();
     look_up(u_first + 32 * W);
 
+    const Shape<T> shape(x, row);
     h8 qh[KC], ql[kSplit ? KC : 1];
     float to_log2;  // not negative: the scale's sign goes into the rows
     {
@@ -143,8 +144,9 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
         top = max_halves(top);
         const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 127);
         const float up = copysignf(__uint_as_float((unsigned)(127 + 14 - e) << 23), a.scale);
-        to_log2 = __uint_as_float((unsigned)(127 - 14 + e) << 23) *
-                  (x.cap > 0.0f ? fabsf(a.scale) / x.cap : fabsf(a.scale) * kLog2e);
+        to_log2 = shape.held(
+            __uint_as_float((unsigned)(127 - 14 + e) << 23) *
+            (x.cap > 0.0f ? shape.held(fabsf(a.scale) / x.cap) : fabsf(a.scale) * kLog2e));
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
 #pragma unroll
@@ -156,7 +158,6 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
             }
     }
 
-    const Shape<T> shape(x, row);
     f16v acc[DT] = {};
     float m = neg_inf(), l = 0.0f;
     // The accumulated values are in units of 2^(lg_run - 15), lg_run the

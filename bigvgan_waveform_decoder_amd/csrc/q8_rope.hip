@@ -10,8 +10,8 @@
 // The angle is taken in 64 bits: p f_i loses whole turns in 32 for far
 // positions.  Quarter turns d = p (2 f_i / pi) are split into rint(d) (whose
 // low two bits choose the quadrant) and a rest in [-1/2, 1/2], exact in 64
-// bits; cosine and sine of the rest are Taylor sums, 1.5 last places off at
-// most.
+// bits; cosine and sine of the rest are Taylor sums: with the rest's rounding
+// to float32 under 4 2^-24 off.
 #include <algorithm>
 #include <type_traits>
 

@@ -665,8 +665,9 @@ int avae_attn_q8(const void* q, long long q_tok, long long q_head, int q_heads, 
  * the other dims stay.  The angle is taken in 64 bits: right to float32's
  * rounding for positions below 2^24 and frequencies up to 1, and to 2e-7 for
  * any below 2^29.
- *   freq: DEVICE, [rot / 2] float32, radians a position, up to 2^16; rot:
- *   even, 0 (nothing is turned) up to the head's dims; amp: finite.
+ *   freq: DEVICE, [rot / 2] float32, radians a position, at most 2^16 in
+ *   magnitude; rot: even, 0 (nothing is turned) up to the head's dims; amp:
+ *   finite.
  */
 typedef struct avae_rope {
     const float* freq;

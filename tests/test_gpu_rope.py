@@ -69,6 +69,35 @@ def test_turned_heads(dim, rot, interleaved, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim,rot,interleaved", [(64, 64, False), (128, 50, True), (96, 96, False)])
+def test_turned_heads_at_odd_places(dim, rot, interleaved, dtype):
+    """Heads that start at an odd element, a token's stride odd too, and a
+    cache write of such keys."""
+    from bigvgan_waveform_decoder_amd import avae
+    torch = _t()
+    announce(f"qk_norm_rope at odd places dim {dim} rot {rot} {dtype}")
+    rng = np.random.default_rng(dim)
+    wide, f = _typed(rng.normal(size=(33, 3 * dim + 7)), dtype)
+    x, xf = (t[:, 5:5 + 3 * dim].reshape(33, 3, dim) if isinstance(t, np.ndarray)
+             else t[:, 5:5 + 3 * dim].unflatten(1, (3, dim)) for t in (wide, f))
+    w = (1 + 0.3 * rng.normal(size=dim)).astype(np.float32)
+    rope, args = avae.Rope(_dev(_freq(rot // 2)), interleaved), dict(cu=_dev(_cu([33])), lens=_dev(np.array([50], np.int32)))
+    want = X.turn(xf, np.arange(17, 50), _freq(rot // 2), interleaved, 1.0, w)
+    got, _ = avae.qk_norm_rope(x, None, rope, _dev(w), **args)
+    assert _near(_np(got), *want, dtype)
+    if dim in (64, 128):
+        c = Cache(3, [50], 3, dim, 16)
+        dev = c.upload()
+        c.avae.kv_write_rope_q8(dev, x, x, _dev(c.table), args["cu"], args["lens"], rope, k_weight=_dev(w))
+        _written(c, _cu([33]), None, *want, (c.k8.copy(), c.ks.copy()))
+    # in place, what lies between stays
+    before = wide.clone()
+    avae.qk_norm_rope(x, None, rope, _dev(w), inplace=True, **args)
+    assert _near(_np(x), *want, dtype)
+    assert torch.equal(wide[:, :5], before[:, :5]) and torch.equal(wide[:, 5 + 3 * dim:], before[:, 5 + 3 * dim:])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_turned_by_given_positions(dtype):
     """Positions beside, before and far after the rows' places; the same ones
     twice; with sequences and without."""

@@ -249,3 +249,60 @@ def test_offsets_that_do_not_lie_in_the_rows(rows):
                           0.125, **kw)[0]
         assert np.abs(_np(out)[:rows] - ref).max() <= 1e-4
         assert (_np(out)[rows:] == 7.0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 9, 40, 100, 300])
+def test_bounds_on_lengths_far_past_them(rows):
+    """max_len at the most that a table may cover, and short sequences: the
+    chunks that it is cut into start past every key."""
+    from bigvgan_waveform_decoder_amd import avae
+    torch = _t()
+    announce(f"attn_rules_q8 max_len 2^29, {rows} rows")
+    lens = [700, 301]
+    new = [rows, 1]
+    c = Cache(64, lens, 2, 64, 256)
+    c.poison_unused()
+    wide = torch.full((2, 1 << 21), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = _dev(c.table)
+    q, qf = _typed(np.random.default_rng(1).normal(size=(rows + 1, 4, 64)), "f32")
+    dev, cu, n = c.upload(), _dev(_cu(new)), _dev(c.lens)
+    tree = _dev(X.tree_words([[i] for i in range(rows)] + [[0]], 10))
+    pre = np.array([100, 50], np.int32)
+    for kw in (dict(cap=9.0), dict(window=70, prefix=pre), dict(window=1 << 28, prefix=pre), dict(lines=1)):
+        if "lines" in kw:
+            kw = dict(lines=[[i] for i in range(rows)] + [[0]])
+            out = avae.attn_tree_q8(q, dev, wide, cu, n, tree, max_q=rows, max_len=1 << 29)
+        else:
+            on = {k: _dev(v) if isinstance(v, np.ndarray) else v for k, v in kw.items()}
+            out = avae.attn_rules_q8(q, dev, wide, cu, n, max_q=rows, max_len=1 << 29, **on)
+        ref = X.attention(qf, c.k8, c.ks, c.v8, c.vs, c.table, _cu(new), lens, 256, 0.125, **kw)[0]
+        assert np.abs(_np(out) - ref).max() <= 1e-4
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_rows_than_tokens_with_windows_and_prefixes(dtype):
+    """Rows before their sequence's first token see nothing, not the prefix."""
+    announce(f"attn_rules_q8 more rows than tokens {dtype}")
+    for new, lens in (([5, 2], [3, 40]), ([40, 3], [30, 2]), ([150], [100]), ([3], [0])):
+        c = Cache(65, lens, 2, 64, 16)
+        c.poison_unused()
+        for window in (0, 2, 64):
+            _check(c, new, 4, dtype, 1, window=window, prefix=np.full(len(new), 7, np.int32), cap=5.0)
+        _check(c, new, 4, dtype, 2, lines=X.lineage(_parents(np.random.default_rng(3), new), _cu(new)))
+
+
+def test_factors_past_float32_under_a_cap():
+    """Scales and caps whose quotient leaves float32: a key that the query has
+    nothing in common with scores 0 all the same."""
+    announce("attn_rules_q8 factors past float32")
+    for new, lens in (([1], [200]), ([9], [200]), ([60], [200]), ([100], [300])):
+        c = Cache(66, lens, 2, 64, 16)
+        c.k8[:, :, ::3] = 0
+        q = np.random.default_rng(1).normal(size=(sum(new), 4, 64))
+        for scale, cap, gain in ((1e30, 1e-30, 1.0), (1.0, 1e-30, 2.0 ** 120), (-1e30, 1e-30, 1e10)):
+            qf = (q * gain).astype(np.float32)
+            out = c.avae.attn_rules_q8(_dev(qf), c.upload(), _dev(c.table), _dev(_cu(new)), _dev(c.lens),
+                                       scale=scale, cap=cap)
+            # (scores within 1e-30 of each other: the mean of the values)
+            ref = X.attention(qf, c.k8, c.ks, c.v8, c.vs, c.table, _cu(new), lens, 16, scale, cap=cap)[0]
+            assert np.abs(_np(out) - ref).max() <= 1e-4
