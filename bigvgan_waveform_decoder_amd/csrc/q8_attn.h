@@ -1299,14 +1299,14 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
     if (r.mid) {
         const int resident = 256 * mid_residency(dim);
         r.chunk = std::max(round_up_to((r.span * pairs + resident - 1) / resident, step), step);
-        if (seqs <= 64) r.pieces = resident;
+        if (seqs > 1 && seqs <= 64) r.pieces = resident;
     } else if (r.many && rules && r.tiles <= 4) {
         // Drafts over long sequences: cut so that two workgroups a CU have
         // work to the end ([16 x 500 to 24000 keys], drafts of 99 to 192 rows:
         // 315 us cut by the longest sequence alone, 225 so).
         const int resident = 512;
         r.chunk = std::max(round_up_to((r.span * pairs + resident - 1) / resident, step), 256);
-        if (seqs <= 64) r.pieces = resident;
+        if (seqs > 1 && seqs <= 64) r.pieces = resident;
     } else if (r.many) {
         // Split only to give every CU a workgroup, in chunks of 128 keys or
         // more: the joined parts are float32 rows ([4 x 512 rows, 1000 keys,

@@ -50,8 +50,16 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
     if (!ragged_rows(r, b, cu0, n, len)) return;
     const int group = a.q_heads / c.heads, rows = n * group, r0 = tile * 32;
     if (r0 >= rows) return;
-    if (x.pieces) chunk = best_chunk(x, c, r, lane, group, 32, splits, 32 * W);
     const Row row = row_of(a, c, x, b, head, cu0, n, len, r0 + n32);
+    // the row's values, on their way while the chunk is found
+    Pack<T, 16> q_raw[D / 32];
+    {
+        const T* q = (const T*)a.q + (long long)row.tok * a.q_tok +
+                     (long long)row.q_head * a.q_head + 16 * g;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) __builtin_memcpy(q_raw[j].v, q + 32 * j, sizeof(q_raw[j].v));
+    }
+    if (x.pieces) chunk = best_chunk(x, c, r, lane, group, 32, splits, 32 * W);
     const Row row0 = row_of(a, c, x, b, head, cu0, n, len, r0);
     const Row row1 = row_of(a, c, x, b, head, cu0, n, len, min(r0 + 31, rows - 1));
     const int first = a.first ? max(a.first[b], 0) : 0;
@@ -135,12 +143,11 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
     h8 qh[KC], ql[kSplit ? KC : 1];
     float to_log2;  // not negative: the scale's sign goes into the rows
     {
-        const T* q = (const T*)a.q + (long long)row.tok * a.q_tok + (long long)row.q_head * a.q_head;
         float top = 0.0f;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf((float)q[32 * j + 16 * g + i]));
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf((float)q_raw[j].v[i]));
         top = max_halves(top);
         const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 127);
         const float up = copysignf(__uint_as_float((unsigned)(127 + 14 - e) << 23), a.scale);
@@ -151,7 +158,7 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
         for (int j = 0; j < D / 32; ++j)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float v = (float)q[32 * j + 16 * g + i] * up;
+                const float v = (float)q_raw[j].v[i] * up;
                 const _Float16 h = (_Float16)v;
                 qh[2 * j + i / 8][i % 8] = h;
                 if (kSplit) ql[2 * j + i / 8][i % 8] = (_Float16)(v - (float)h);
