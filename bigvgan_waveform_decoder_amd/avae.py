@@ -951,17 +951,6 @@ class _Env:
         """The raw stream to launch on: the current one of the tensor's device."""
         return self.raw_stream(t.get_device())
 
-    def launch(self, dev, f, *args):
-        """f(*args, stream) on the current stream of device number `dev`,
-        which is made the current device meanwhile."""
-        if dev == self.device():
-            rc = f(*args, self.raw_stream(dev))
-        else:
-            with _torch().cuda.device(dev):
-                rc = f(*args, self.raw_stream(dev))
-        if rc:
-            _check(rc)
-
 
 _env: Optional[_Env] = None
 
@@ -1106,13 +1095,18 @@ class KvCacheQ8:
         E = _q8()
         if k.dim() != 4:
             raise ValueError(f"k: expected [n_pages, heads, page, dim], got {tuple(k.shape)}")
-        shape = k.shape
+        shape, i8, f32 = k.shape, E.int8, E.float32
         scales = shape[:2]
-        for name, t, dtype, want in (("k", k, E.int8, shape), ("v", v, E.int8, shape),
-                                     ("k_scale", k_scale, E.float32, scales),
-                                     ("v_scale", v_scale, E.float32, scales)):
-            if not t.is_cuda or t.dtype != dtype or t.shape != want or not t.is_contiguous():
-                _bad(t, name, dtype, f"{tuple(want)}")
+        if not (k.is_cuda and k.dtype is i8 and k.is_contiguous()):
+            _bad(k, "k", i8, f"{tuple(shape)}")
+        if not (v.is_cuda and v.dtype is i8 and v.shape == shape and v.is_contiguous()):
+            _bad(v, "v", i8, f"{tuple(shape)}")
+        if not (k_scale.is_cuda and k_scale.dtype is f32 and k_scale.shape == scales
+                and k_scale.is_contiguous()):
+            _bad(k_scale, "k_scale", f32, f"{tuple(scales)}")
+        if not (v_scale.is_cuda and v_scale.dtype is f32 and v_scale.shape == scales
+                and v_scale.is_contiguous()):
+            _bad(v_scale, "v_scale", f32, f"{tuple(scales)}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         _, self.heads, self.page, self.dim = shape
         self.c = avae_kv_q8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
@@ -1246,11 +1240,13 @@ class Rope:
     __slots__ = ("freq", "rot", "c", "ref")
 
     def __init__(self, freq, interleaved: bool = False, amp: float = 1.0):
-        if freq.dim() != 1 or freq.shape[0] < 1:
-            raise ValueError(f"freq: expected [rot / 2], got {tuple(freq.shape)}")
-        p = _vec(freq, "freq", freq.shape[0], _q8().float32)
-        self.freq, self.rot = freq, 2 * freq.shape[0]
-        self.c = avae_rope(p, self.rot, 1 if interleaved else 0, amp)
+        shape = freq.shape
+        if len(shape) != 1 or shape[0] < 1:
+            raise ValueError(f"freq: expected [rot / 2], got {tuple(shape)}")
+        if not (freq.is_cuda and freq.dtype is _q8().float32 and freq.is_contiguous()):
+            _bad(freq, "freq", _q8().float32, f"[{shape[0]}]")
+        self.freq, self.rot = freq, 2 * shape[0]
+        self.c = avae_rope(freq.data_ptr(), self.rot, 1 if interleaved else 0, amp)
         self.ref = ctypes.addressof(self.c)
 
     @classmethod
@@ -1333,10 +1329,15 @@ def qk_norm_rope(q, k, rope: Optional[Rope], q_weight=None, k_weight=None, eps: 
             return qk_norm_rope(q, k, rope, q_weight, k_weight, eps, positions, cu, lens, max_rows,
                                 inplace)
     E = _q8()
+    dev = q.get_device()
+    if dev >= 0 and dev != E.device():
+        with _torch().cuda.device(dev):
+            return qk_norm_rope(q, k, rope, q_weight, k_weight, eps, positions, cu, lens, max_rows,
+                                inplace)
     if q.dim() != 3:
         raise ValueError(f"q: expected [tokens, heads, dim], got {tuple(q.shape)}")
     total, heads, dim = q.shape
-    dtype, dev, f32 = q.dtype, q.get_device(), E.float32
+    dtype, f32 = q.dtype, E.float32
     code = E.code(dtype)
     pq, q_tok, q_head = _heads_at(q, "q", dtype, total, heads, dim, dev)
     device = q.device
@@ -1358,14 +1359,16 @@ def qk_norm_rope(q, k, rope: Optional[Rope], q_weight=None, k_weight=None, eps: 
     if (cu is None) != (lens is None):
         raise ValueError("cu and lens are given together or not at all")
     rows = None if cu is None else _rows_at(E, None, cu, lens, total, max_rows, dev)
-    E.launch(dev, E.qk, pq, q_tok, q_head, heads,
-             None if q_weight is None else _vec_at(q_weight, "q_weight", dim, f32, dev),
-             pk, k_tok, k_head, k_heads,
-             None if k_weight is None else _vec_at(k_weight, "k_weight", dim, f32, dev), dim, code,
-             eps, _freq_at(rope, dev),
-             None if positions is None else _vec_at(positions, "positions", total, E.int32, dev),
-             None if rows is None else ctypes.addressof(rows), total, pqo, qo_tok, qo_head, pko,
-             ko_tok, ko_head)
+    rc = E.qk(pq, q_tok, q_head, heads,
+              None if q_weight is None else _vec_at(q_weight, "q_weight", dim, f32, dev),
+              pk, k_tok, k_head, k_heads,
+              None if k_weight is None else _vec_at(k_weight, "k_weight", dim, f32, dev), dim, code,
+              eps, _freq_at(rope, dev),
+              None if positions is None else _vec_at(positions, "positions", total, E.int32, dev),
+              None if rows is None else ctypes.addressof(rows), total, pqo, qo_tok, qo_head, pko,
+              ko_tok, ko_head, E.raw_stream(dev))
+    if rc:
+        _check(rc)
     return q_out, k_out
 
 
@@ -1379,22 +1382,35 @@ def kv_write_rope_q8(cache: KvCacheQ8, k, v, table, cu, lens, rope: Optional[Rop
             return kv_write_rope_q8(cache, k, v, table, cu, lens, rope, k_weight, eps, positions,
                                     max_new)
     E = _q8()
-    total, dtype, dev = k.shape[0], k.dtype, k.get_device()
+    dev = k.get_device()
+    if dev >= 0 and dev != E.device():
+        with _torch().cuda.device(dev):
+            return kv_write_rope_q8(cache, k, v, table, cu, lens, rope, k_weight, eps, positions,
+                                    max_new)
+    total, dtype = k.shape[0], k.dtype
     heads, dim = cache.heads, cache.dim
     _same_device(cache, dev)
     rows = _rows_at(E, table, cu, lens, total, max_new, dev)
-    E.launch(dev, E.write_rope, *_heads_at(k, "k", dtype, total, heads, dim, dev),
-             *_heads_at(v, "v", dtype, total, heads, dim, dev), E.code(dtype),
-             None if k_weight is None else _vec_at(k_weight, "k_weight", dim, E.float32, dev), eps,
-             _freq_at(rope, dev),
-             None if positions is None else _vec_at(positions, "positions", total, E.int32, dev),
-             cache.ref, ctypes.addressof(rows))
+    rc = E.write_rope(
+        *_heads_at(k, "k", dtype, total, heads, dim, dev),
+        *_heads_at(v, "v", dtype, total, heads, dim, dev), E.code(dtype),
+        None if k_weight is None else _vec_at(k_weight, "k_weight", dim, E.float32, dev), eps,
+        _freq_at(rope, dev),
+        None if positions is None else _vec_at(positions, "positions", total, E.int32, dev),
+        cache.ref, ctypes.addressof(rows), E.raw_stream(dev))
+    if rc:
+        _check(rc)
 
 
 def _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, causal, window, first, rules,
                 return_lse):
     E = _q8()
-    dim, dtype, dev = cache.dim, q.dtype, q.get_device()
+    dev = q.get_device()
+    if dev >= 0 and dev != E.device():
+        with _torch().cuda.device(dev):
+            return _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, causal, window, first,
+                               rules, return_lse)
+    dim, dtype = cache.dim, q.dtype
     code = E.code(dtype)
     total = q.shape[0]
     pq, tok, head = _heads_at(q, "q", dtype, total, None, dim, dev)
@@ -1410,11 +1426,13 @@ def _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, causal, window
     lse = E.mat(total, heads, E.float32, device) if return_lse else None
     need = E.rules_ws(cache.ref, pr, heads, code, max_len, window, px)
     ws = E.vec(need, E.uint8, device) if need else None
-    E.launch(dev, E.rules, pq, tok, head, heads, code, cache.ref, pr,
-             None if first is None else _vec_at(first, "first", rows.seqs, E.int32, dev), max_len,
-             dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, px,
-             out.data_ptr(), None if lse is None else lse.data_ptr(),
-             None if ws is None else ws.data_ptr(), need)
+    rc = E.rules(pq, tok, head, heads, code, cache.ref, pr,
+                 None if first is None else _vec_at(first, "first", rows.seqs, E.int32, dev),
+                 max_len, dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, px,
+                 out.data_ptr(), None if lse is None else lse.data_ptr(),
+                 None if ws is None else ws.data_ptr(), need, E.raw_stream(dev))
+    if rc:
+        _check(rc)
     return (out, lse) if return_lse else out
 
 
@@ -1455,13 +1473,18 @@ def tree_mask(parents, cu, lens, max_rows: Optional[int] = None, stream=None):
     if parents.dim() != 1:
         raise ValueError(f"parents: expected [tokens], got {tuple(parents.shape)}")
     total, dev, device = parents.shape[0], parents.get_device(), parents.device
+    if dev >= 0 and dev != E.device():
+        with _torch().cuda.device(dev):
+            return tree_mask(parents, cu, lens, max_rows)
     p = _vec_at(parents, "parents", total, E.int32, dev)
     rows = _rows_at(E, None, cu, lens, total, max_rows, dev)
     words = (rows.max_rows + 31) // 32
     mask = E.mat(total, words, E.int32, device)
     positions = E.vec(total, E.int32, device)
-    E.launch(dev, E.tree, p, ctypes.addressof(rows), words, mask.data_ptr(), words,
-             positions.data_ptr())
+    rc = E.tree(p, ctypes.addressof(rows), words, mask.data_ptr(), words, positions.data_ptr(),
+                E.raw_stream(dev))
+    if rc:
+        _check(rc)
     return mask, positions
 
 
