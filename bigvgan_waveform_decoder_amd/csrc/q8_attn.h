@@ -1267,11 +1267,11 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
     r.many = rows > 32;
     // With rules, the kernel for drafts between them.  This one / the others in
     // us, bfloat16, 12 over 4 heads of 128, drafts of one size: [16 x 12000
-    // keys] 24 rows 47 / 83, 48 rows 67 / 79, 96 rows 108 / 95, 192 rows 178 /
-    // 160, 258 rows 236 / 233; [64 x 4000] 56 / 100, 94 / 108, 148 / 126, 248 /
-    // 217; [16 x 500 to 24000] 48 rows 121 / 117, 96 rows 146 / 156, 192 rows
-    // 212 / 284, drafts of 99 to 192 rows 188 / 225; heads of 256, [16 x
-    // 12000], 96 rows 139 / 168, 192 rows 229 / 261.
+    // keys] 24 rows 49 / 83, 48 rows 75 / 79, 96 rows 101 / 95, 192 rows 172 /
+    // 160, 258 rows 236 / 233; [64 x 4000] 24 rows 56 / 100, 96 rows 138 / 126;
+    // [16 x 500 to 24000] 48 rows 97 / 117, 96 rows 142 / 156, 192 rows 222 /
+    // 284, drafts of 99 to 192 rows 184 / 225; [16 x 12000], 96 rows of heads
+    // of 64 75 / 75, of 256 102 / 168, float32 124 / 130.
     r.mid = rules && rows > 16 && rows <= 192;
     const int height = r.mid ? 32 : r.many ? 32 * kWaves : 16;
     const int step = r.many && !r.mid ? 64 : 32 * kWaves;
@@ -1297,6 +1297,8 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
         return r;
     }
     if (r.mid) {
+        // One resident round ([16 x 500 to 24000 keys], drafts of 99 to 192
+        // rows: 184 us; two workgroups a CU 193, four 196).
         const int resident = 256 * mid_residency(dim);
         r.chunk = std::max(round_up_to((r.span * pairs + resident - 1) / resident, step), step);
         if (seqs > 1 && seqs <= 64) r.pieces = resident;

@@ -11,11 +11,20 @@
 // that join.
 //
 // The tiles of a sequence's rows read the same keys: they go to one XCD, one
-// after the other, and find them in its L2.
+// after the other, and find them in its L2 (the memory traffic of three tiles
+// is one's).
+//
+// One tile is bound by HBM ([16 sequences of 12000 keys, 4 heads of 128], 24
+// rows: 49 us, 4.0 TB/s), more by their vector instructions, 340 for 32 rows
+// and 32 keys, half of them the conversion of keys and values (96 rows 101 us:
+// the vector units are busy 55%, the matrix cores 15% of the cycles; 384
+// accesses of the first cache a step take half of them).  Three waves a SIMD:
+// with the rows' operands in registers there are two (96 rows 110 us); two
+// tiles a wave, which share the conversion, leave one (147).
 #pragma once
 
-// Waves a SIMD of the kernel below.
-constexpr int mid_residency(int dim) { return dim > 128 ? 1 : 2; }
+// Waves a SIMD of the kernel below: what its registers allow.
+constexpr int mid_residency(int dim) { return dim > 128 ? 2 : 3; }
 // Waves of its workgroups where they take all the keys of their rows: what
 // fits in LDS.
 constexpr int mid_wide_waves(int dim) { return dim > 128 ? 4 : 8; }
@@ -32,13 +41,14 @@ __device__ inline Words<(N + 3) / 4> load_bytes(const int8_t* p) {  // N bytes, 
 }
 
 template <typename T, int D, int W>
-__global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
+__global__ __launch_bounds__(64 * W, W > kWaves ? 2 : mid_residency(D)) void attn_q8_mid_kernel(
     AttnQ8 a, CacheQ8 c, Ragged r, AttnRules x, int splits, int chunk, int tiles, float* part) {
     constexpr bool kSplit = sizeof(T) == 4;
     constexpr int KC = D / 16;  // key operands of 16 dims
     constexpr int DT = D / 32;  // output tiles; a lane's values of one key, too
-    constexpr int LD = D + 4;
-    __shared__ __align__(16) float s_out[W * 32 * LD];
+    constexpr int LD = D + 4, JD = 64 + 4;
+    __shared__ __align__(16) h8 s_q[(kSplit ? 2 : 1) * KC * 64];
+    __shared__ __align__(16) float s_out[W * 32 * JD];
     __shared__ float s_m[W * 32], s_l[W * 32];
     const int lane = threadIdx.x & 63, wave = wave_id(), n32 = lane & 31, g = lane >> 5;
     const int pairs = r.seqs * c.heads, tile = (blockIdx.x >> 3) % tiles;
@@ -140,7 +150,8 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
     look_up(u_first + 32 * W);
 
     const Shape<T> shape(x, row);
-    h8 qh[KC], ql[kSplit ? KC : 1];
+    // The rows are the same for all waves: their operands lie in LDS, in the
+    // lanes' order, and leave the registers to another wave.
     float to_log2;  // not negative: the scale's sign goes into the rows
     {
         float top = 0.0f;
@@ -154,16 +165,22 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
         to_log2 = shape.held(
             __uint_as_float((unsigned)(127 - 14 + e) << 23) *
             (x.cap > 0.0f ? shape.held(fabsf(a.scale) / x.cap) : fabsf(a.scale) * kLog2e));
+        if (wave == 0) {
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j)
+            for (int j = 0; j < KC; ++j) {
+                h8 high, low;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float v = (float)q_raw[j].v[i] * up;
-                const _Float16 h = (_Float16)v;
-                qh[2 * j + i / 8][i % 8] = h;
-                if (kSplit) ql[2 * j + i / 8][i % 8] = (_Float16)(v - (float)h);
+                for (int i = 0; i < 8; ++i) {
+                    const float v = (float)q_raw[j / 2].v[j % 2 * 8 + i] * up;
+                    high[i] = (_Float16)v;
+                    low[i] = (_Float16)(v - (float)high[i]);
+                }
+                s_q[64 * j + lane] = high;
+                if (kSplit) s_q[64 * (KC + j) + lane] = low;
             }
+        }
     }
+    __syncthreads();
 
     f16v acc[DT] = {};
     float m = neg_inf(), l = 0.0f;
@@ -179,17 +196,15 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
             vs[h] = next_vs[h];
             there[h] = next_there[h];
         }
+        asm volatile("" ::: "memory");  // (the operands are read anew each step)
         f16v s = {};
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-            const h8 k_lo = to_half8(kw[j].w[0], kw[j].w[1]);
-            const h8 k_hi = to_half8(kw[j].w[2], kw[j].w[3]);
-            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_lo, qh[2 * j], s, 0, 0, 0);
-            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_hi, qh[2 * j + 1], s, 0, 0, 0);
-            if (kSplit) {
-                s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_lo, ql[2 * j], s, 0, 0, 0);
-                s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_hi, ql[2 * j + 1], s, 0, 0, 0);
-            }
+        for (int j = 0; j < KC; ++j) {
+            const h8 kv = to_half8(kw[j / 2].w[j % 2 * 2], kw[j / 2].w[j % 2 * 2 + 1]);
+            s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv, s_q[64 * j + lane], s, 0, 0, 0);
+            if (kSplit)
+                s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kv, s_q[64 * (KC + j) + lane], s, 0, 0,
+                                                           0);
         }
         // (what is asked for past the last step is of no use, and harmless)
         fetch_keys(u0 + 32 * W);
@@ -306,49 +321,55 @@ __global__ __launch_bounds__(64 * W, mid_residency(D)) void attn_q8_mid_kernel(
     }
     // the unit in two halves, since it may be below float32
     const float half = __builtin_amdgcn_exp2f(0.5f * (lg_run - 15.0f));
+    // joined 64 dims at a time
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        constexpr int N = DT < 4 ? DT : 4;
+    for (int d0 = 0; d0 < D; d0 += 64) {
+        constexpr int N = DT < 4 ? DT : 4, EACH = 64 / DT;  // rows of the stacked output tiles
+        if (d0 > 0) __syncthreads();
 #pragma unroll
-        for (int t = 0; t < DT; t += N) {
-            Pack<float, N> o;
+        for (int i = 0; i < 16; ++i) {
+            if (8 * (i >> 2) / EACH != d0 / 64) continue;
+            const int at = DT * (8 * (i >> 2) + 4 * g + (i & 3)) - d0;
 #pragma unroll
-            for (int e = 0; e < N; ++e) o.v[e] = acc[t + e][i] * half * half;
-            *reinterpret_cast<Pack<float, N>*>(s_out + (wave * 32 + n32) * LD +
-                                               DT * (8 * (i >> 2) + 4 * g + (i & 3)) + t) = o;
-        }
-    }
-    __syncthreads();
-    // each thread joins four dims of a row
-    for (int e = threadIdx.x; e < 32 * (D / 4); e += 64 * W) {
-        const int i = e / (D / 4), d = e % (D / 4) * 4;
-        const Row to = row_of(a, c, x, b, head, cu0, n, len, r0 + i);
-        if (!to.live) break;  // rows come in order
-        float top = neg_inf(), sum = 0.0f;
-        for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w * 32 + i]);
-        const float base_m = top == neg_inf() ? 0.0f : top;
-        f4 o = {};
-        for (int w = 0; w < W; ++w) {
-            const float by = chunk_weight(s_m[w * 32 + i], s_l[w * 32 + i], base_m);
-            if (by == 0.0f) continue;
-            sum += by * s_l[w * 32 + i];
-            o += by * *reinterpret_cast<const f4*>(s_out + (w * 32 + i) * LD + d);
-        }
-        const long long out_row = (long long)to.tok * a.q_heads + to.q_head;
-        if (splits > 1) {
-            float* pr = part + (out_row * splits + split) * LD;
-            *reinterpret_cast<f4*>(pr + 4 + d) = o;
-            if (d == 0) {
-                pr[0] = top;
-                pr[1] = sum;
+            for (int t = 0; t < DT; t += N) {
+                Pack<float, N> o;
+#pragma unroll
+                for (int e = 0; e < N; ++e) o.v[e] = acc[t + e][i] * half * half;
+                *reinterpret_cast<Pack<float, N>*>(s_out + (wave * 32 + n32) * JD + at + t) = o;
             }
-        } else {
-            const float by = sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN sum stays NaN
-            Pack<T, 4> y;
+        }
+        __syncthreads();
+        // each thread joins four dims of a row
+        for (int e = threadIdx.x; e < 32 * 16; e += 64 * W) {
+            const int i = e / 16, d = e % 16 * 4;
+            const Row to = row_of(a, c, x, b, head, cu0, n, len, r0 + i);
+            if (!to.live) break;  // rows come in order
+            float top = neg_inf(), sum = 0.0f;
+            for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w * 32 + i]);
+            const float base_m = top == neg_inf() ? 0.0f : top;
+            f4 o = {};
+            for (int w = 0; w < W; ++w) {
+                const float by = chunk_weight(s_m[w * 32 + i], s_l[w * 32 + i], base_m);
+                if (by == 0.0f) continue;
+                sum += by * s_l[w * 32 + i];
+                o += by * *reinterpret_cast<const f4*>(s_out + (w * 32 + i) * JD + d);
+            }
+            const long long out_row = (long long)to.tok * a.q_heads + to.q_head;
+            if (splits > 1) {
+                float* pr = part + (out_row * splits + split) * LD;
+                *reinterpret_cast<f4*>(pr + 4 + d0 + d) = o;
+                if (d0 + d == 0) {
+                    pr[0] = top;
+                    pr[1] = sum;
+                }
+            } else {
+                const float by = sum == 0.0f ? 0.0f : 1.0f / sum;  // a NaN sum stays NaN
+                Pack<T, 4> y;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y.v[j] = round_to<T>(o[j] * by);
-            *reinterpret_cast<Pack<T, 4>*>((T*)a.out + out_row * D + d) = y;
-            if (a.lse && d == 0) a.lse[out_row] = lse_of(top, sum);
+                for (int j = 0; j < 4; ++j) y.v[j] = round_to<T>(o[j] * by);
+                *reinterpret_cast<Pack<T, 4>*>((T*)a.out + out_row * D + d0 + d) = y;
+                if (a.lse && d0 + d == 0) a.lse[out_row] = lse_of(top, sum);
+            }
         }
     }
 }
