@@ -1303,6 +1303,9 @@ def _rows_at(E, table, cu, lens, total: int, max_rows: Optional[int], dev: int):
                        total if max_rows is None or max_rows > total else max_rows)
 
 
+_MOST = 2 ** 31 - 1
+
+
 def _same_device(cache, dev: int):
     if cache.k.get_device() != dev:
         raise ValueError(f"the cache is on device {cache.k.get_device()}, the first tensor on {dev}")
@@ -1420,6 +1423,8 @@ def _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, causal, window
     pr, px = ctypes.addressof(rows), ctypes.addressof(rules)
     if max_len is None:
         max_len = rows.table_cols * cache.page
+    if window > _MOST or max_len > _MOST:  # ctypes would take their low 32 bits
+        window, max_len = min(window, _MOST), min(max_len, _MOST)
     if rules.max_prefix < 0:
         rules.max_prefix = max_len
     out = E.heads(total, heads, dim, dtype, device)
@@ -1456,7 +1461,7 @@ def attn_rules_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = N
     rules = avae_attn_rules(
         cap, None if slopes is None else _vec_at(slopes, "slopes", q.shape[1], E.float32, dev),
         None if prefix is None else _vec_at(prefix, "prefix", lens.shape[0], E.int32, dev),
-        -1 if max_prefix is None else max_prefix, None, 0, 0)
+        -1 if max_prefix is None else min(max_prefix, _MOST), None, 0, 0)
     return _attn_rules(q, cache, table, cu, lens, max_q, max_len, scale, causal, window, first,
                        rules, return_lse)
 

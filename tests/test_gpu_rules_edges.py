@@ -306,3 +306,24 @@ def test_factors_past_float32_under_a_cap():
             # (scores within 1e-30 of each other: the mean of the values)
             ref = X.attention(qf, c.k8, c.ks, c.v8, c.vs, c.table, _cu(new), lens, 16, scale, cap=cap)[0]
             assert np.abs(_np(out) - ref).max() <= 1e-4
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_windows_and_prefixes_past_32_bits(rows):
+    """Bounds that no 32-bit number holds: as the largest that one does, not as
+    their low bits."""
+    rng = np.random.default_rng(21)
+    c = Cache(53, [900, 300], 2, 64, 16)
+    c.upload()
+    q = _typed(rng.normal(size=(2 * rows, 8, 64)), "f32")[0]
+    args = (q, c.dev, _dev(c.table), _dev(_cu([rows, rows])), _dev(c.lens))
+    announce(f"attn_rules_q8 window, max_prefix past 32 bits, {rows} rows")
+    avae = c.avae
+    prefix = _dev(np.array([700, 200], np.int32))
+    whole = avae.attn_rules_q8(*args, max_q=rows, cap=10.0)
+    assert _t().equal(whole, avae.attn_rules_q8(*args, max_q=rows, cap=10.0, window=2 ** 32 + 3))
+    near = avae.attn_rules_q8(*args, max_q=rows, window=50, prefix=prefix, max_prefix=2 ** 31 - 1)
+    far = avae.attn_rules_q8(*args, max_q=rows, window=50, prefix=prefix, max_prefix=2 ** 32 + 3)
+    assert _t().equal(near, far)
+    with pytest.raises(avae.AvaeError):
+        avae.attn_rules_q8(*args, max_q=rows, max_len=2 ** 32 + 3)
