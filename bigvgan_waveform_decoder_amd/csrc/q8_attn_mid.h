@@ -20,7 +20,11 @@
 // the vector units are busy 55%, the matrix cores 15% of the cycles; 384
 // accesses of the first cache a step take half of them).  Three waves a SIMD:
 // with the rows' operands in registers there are two (96 rows 110 us); two
-// tiles a wave, which share the conversion, leave one (147).
+// tiles a wave, which share the conversion and the accesses, leave two at best
+// (144): a wave's step is a chain of instructions, which more waves hide
+// better than fewer instructions shorten it.  Nor do fewer accesses help: keys
+// loaded line by line and turned through LDS take as long (heads of 64, 96
+// rows: 74 us either way).
 #pragma once
 
 // Waves a SIMD of the kernel below: what its registers allow.
