@@ -224,8 +224,9 @@ struct Shape {
           quick(sizeof(T) < 4 && x.cap > 0.0f && x.cap <= 256.0f) {
         if (sloped) slope = x.slopes[r.q_head] * kLog2e;
     }
-    // (a scale that is not finite stays with the score whatever the cap, and
-    // under one a factor past float32 is held: 0 times an infinity is NaN)
+    // The factor of a page's scores.  A scale that is not finite makes them NaN
+    // whatever the cap (`held` alone would make a number of a NaN), and under
+    // one a factor past float32 is held: 0 times an infinity is NaN.
     __device__ float by(float ks, float to_log2) const {
         return finite(ks) ? held(ks * to_log2) : nan();
     }
@@ -873,8 +874,6 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
         }
         Group to = next;
         to.ks = to.on ? to.ks : 0.0f;
-        if constexpr (kRules<R>)
-            if (!finite(to.ks)) to.ks = nan();  // stays with the score whatever the cap
         to.vs = to.on ? to.vs : 0.0f;
         to.on |= finite(to.vs) ? 0 : 2;
         to.lg_vs = finite(to.vs) ? __builtin_amdgcn_logf(to.vs) : neg_inf();
@@ -1010,7 +1009,10 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
                     scores(s, kp + 32 * h0 * KLD);
 #pragma unroll
                     for (int u = 0; u < 2 * HS; ++u) {
-                        by[u] = gp[2 * h0 + u].ks * to_log2;
+                        if constexpr (kRules<R>)
+                            by[u] = shape.by(gp[2 * h0 + u].ks, to_log2);
+                        else
+                            by[u] = gp[2 * h0 + u].ks * to_log2;
                         lg_vs[u] = gp[2 * h0 + u].lg_vs;
                     }
                     if (h0 == 0) {
@@ -1019,12 +1021,9 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
                     }
                     if constexpr (kRules<R>) {
 #pragma unroll
-                        for (int h = 0; h < HS; ++h) {
-                            by[2 * h] = shape.held(by[2 * h]);
-                            by[2 * h + 1] = shape.held(by[2 * h + 1]);
+                        for (int h = 0; h < HS; ++h)
                             shape_scores(shape, s[h], by + 2 * h,
                                          (float)(row.pos - (t0 + 32 * (h0 + h) + 4 * g)));
-                        }
                     }
                     if (!seen) {
                         // What is hidden from a row goes into its scores, and

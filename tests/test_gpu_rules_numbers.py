@@ -1,0 +1,62 @@
+"""Attention with rules where numbers leave float32 or its middle, in every
+kernel (few rows, drafts, many rows) and type: scales of pages that are not
+finite under a cap."""
+import numpy as np
+import pytest
+
+from tests import rules_reference as X
+from tests.gpu_util import announce
+from tests.test_gpu_attn_rules import _slopes
+from tests.test_gpu_q8 import ROUND, U, Cache, _cu, _dev, _np, _typed
+
+pytestmark = pytest.mark.gpu
+
+# rows a cache head, two query heads each: 2 (few rows), 80 (drafts), 400 (many rows)
+ROWS = [1, 40, 200]
+TYPES = ["f32", "bf16", "f16"]
+
+
+def _call(c, q, new, **kw):
+    on = {k: _dev(v) if isinstance(v, np.ndarray) else v for k, v in kw.items()}
+    out, lse = c.avae.attn_rules_q8(q, c.upload(), _dev(c.table), _dev(_cu(new)), _dev(c.lens),
+                                    max_q=max(new), return_lse=True, **on)
+    return _np(out), _np(lse)
+
+
+# ------------------------------------------------------------------ what is not finite
+
+@pytest.mark.parametrize("cap", [10.0, 300.0])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", ROWS)
+def test_scales_that_are_not_finite_under_a_cap(rows, dtype, cap):
+    """The rows that see such a page are NaN, in lse too, whatever the cap
+    makes of an infinite score; the others as if it were not there."""
+    announce(f"attn_rules_q8 scales not finite, {rows} rows, cap {cap} {dtype}")
+    length = 500
+    q, qf = _typed(np.random.default_rng(1).normal(size=(rows, 4, 64)), dtype)
+    pos = np.arange(length - rows, length)
+    key = np.arange(length)
+    pre = np.array([50], np.int32)
+    window = dict(window=40, prefix=pre, slopes=_slopes(4))
+    for what, value in (("ks", np.nan), ("ks", np.inf), ("vs", np.nan), ("vs", np.inf)):
+        for col, kw in ((1, window), ((length - 1) // 16, window), (7, {}), ((length - 1) // 16, {}),
+                        ((length - rows // 2) // 16, {})):
+            c = Cache(12, [length], 2, 64, 16)
+            c.poison_unused()
+            getattr(c, what)[c.table[0, col], 1] = value
+            out, lse = _call(c, q, [rows], cap=cap, **kw)
+            seen = key <= pos[:, None]
+            if kw:
+                seen = seen & (key > pos[:, None] - 40) | (key < 50)
+            see = seen[:, 16 * col:16 * col + 16].any(1)
+            want = np.repeat(see[:, None], 4, 1) & (np.arange(4) >= 2)
+            assert np.array_equal(np.isnan(out).all(2), want)
+            assert np.array_equal(np.isnan(out).any(2), want)
+            assert np.array_equal(np.isnan(lse), want)
+            getattr(c, what)[c.table[0, col], 1] = 0.01
+            ref, rlse, weight, _, _ = X.attention(qf, c.k8, c.ks, c.v8, c.vs, c.table, _cu([rows]), [length],
+                                                  16, 0.125, cap=cap, **kw)
+            # (what the page's value is instead is in the reference of no row compared)
+            assert np.all(np.abs(out - ref)[~want] <= (2.0 ** -9 if dtype == "bf16" else 2.0 ** -10) * weight[~want]
+                          + ROUND[dtype][0] * np.abs(ref[~want]) + 1e-30)
+            assert np.all(np.abs(lse - rlse)[~want] <= 1e-3)
