@@ -226,12 +226,13 @@ struct Shape {
     }
     // The factor of a page's scores.  A scale that is not finite makes them NaN
     // whatever the cap (`held` alone would make a number of a NaN), and under
-    // one a factor past float32 is held: 0 times an infinity is NaN.
+    // one a factor past float32 is held: 0 times an infinity is NaN.  (At a
+    // third of float32's largest: the quick cap takes it 2 log2 e times.)
     __device__ float by(float ks, float to_log2) const {
         return finite(ks) ? held(ks * to_log2) : nan();
     }
     __device__ float held(float x) const {
-        return capped ? fminf(fmaxf(x, -3.4e38f), 3.4e38f) : x;
+        return capped ? fminf(fmaxf(x, -1.1e38f), 1.1e38f) : x;
     }
     // The cap,
     // of s = 2 y log2 e, over 2 cap

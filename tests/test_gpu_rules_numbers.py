@@ -1,6 +1,6 @@
 """Attention with rules where numbers leave float32 or its middle, in every
 kernel (few rows, drafts, many rows) and type: scales of pages that are not
-finite under a cap."""
+finite under a cap, factors past float32."""
 import numpy as np
 import pytest
 
@@ -60,3 +60,34 @@ def test_scales_that_are_not_finite_under_a_cap(rows, dtype, cap):
             assert np.all(np.abs(out - ref)[~want] <= (2.0 ** -9 if dtype == "bf16" else 2.0 ** -10) * weight[~want]
                           + ROUND[dtype][0] * np.abs(ref[~want]) + 1e-30)
             assert np.all(np.abs(lse - rlse)[~want] <= 1e-3)
+
+
+# ------------------------------------------------------------------ caps
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", ROWS)
+def test_factors_past_float32_with_large_scales(rows, dtype):
+    """Key scales over 0.35 and quotients scale * |q| / cap past float32: a key
+    that the query has nothing in common with scores 0, no NaN.  All scores
+    lie within 1e-30 of each other, so the output is the values' mean: off by
+    the probabilities' rounding (2^-11 in bfloat16, 2^-21 in the others'
+    parts), by float32 sums of 300 terms in parts of 8 and the weights' 64
+    roundings, and by its own."""
+    announce(f"attn_rules_q8 large scales under a small cap, {rows} rows {dtype}")
+    length = 300
+    c = Cache(66, [length], 2, 64, 16)
+    c.k8[:, :, ::3] = 0
+    c.ks[:] = np.random.default_rng(3).uniform(0.36, 3.0, size=c.ks.shape)
+    q = np.random.default_rng(1).normal(size=(rows, 4, 64))
+    q = q / np.abs(q).max(2, keepdims=True)
+    for scale, cap, gain in ((1e30, 1e-30, 60000.0), (-1e30, 1e-30, 33000.0), (3e38, 1e-30, 50000.0),
+                             (1e38, 0.5, 60000.0)):
+        dq, qf = _typed(q * gain, dtype)
+        out, lse = _call(c, dq, [rows], scale=scale, cap=cap)
+        if cap < 1e-3:
+            ref, rlse, weight, _, _ = X.attention(qf, c.k8, c.ks, c.v8, c.vs, c.table, _cu([rows]), [length], 16,
+                                                  scale, cap=cap)
+            tol = (2 * (length / 8 + 64) * U + (2.0 ** -11 if dtype == "bf16" else 2.0 ** -21)) * weight
+            assert np.all(np.abs(out - ref) <= tol + ROUND[dtype][0] * np.abs(ref) + ROUND[dtype][1])
+            assert np.all(np.abs(lse - rlse) <= (length / 8 + 64) * U + 8 * U * np.abs(rlse))
+        assert np.isfinite(out).all() and np.isfinite(lse).all()
