@@ -192,14 +192,15 @@ __device__ inline unsigned keys_seen(const Row& r, const AttnRules& x, int start
     return seen | (ones_below(r.pre - t) & ~ones_below(r.first - t));
 }
 
-// tanh(y): (1 - e) / (1 + e) with e = exp(-2 |y|) is 2^-24 off, which float32
-// outputs would feel for small scores under a large cap (the cap multiplies
-// it): they take the odd series there.
-template <typename T>
-__device__ inline float tanh_of(float y) {
+// tanh(y): (1 - e) / (1 + e) with e = exp(-2 |y|) is 2^-24 off, and a cap
+// multiplies that.  `rough`: let it (16-bit types under caps up to 256, whose
+// own rounding hides it); else small |y| take the odd series, right to y's own
+// rounding, so that a score far below its cap stays what it is.  (Without it a
+// cap of 1e6 made bfloat16 scores 1.3% wrong, one of 1e30 all of them 0.)
+__device__ inline float tanh_of(float y, bool rough) {
     const float e = __builtin_amdgcn_exp2f(fabsf(y) * (-2.0f * kLog2e));
     const float far = copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), y);
-    if constexpr (sizeof(T) < 4) return far;
+    if (rough) return far;
     const float z = y * y;
     float p = fmaf(z, -8.8632355e-3f, 2.1869489e-2f);
     p = fmaf(z, p, -5.3968254e-2f);
@@ -240,7 +241,7 @@ struct Shape {
         return __builtin_amdgcn_rcpf(-1.0f - __builtin_amdgcn_exp2f(s));
     }
     // of s = y
-    __device__ float cap_whole(float s) const { return cap * tanh_of<T>(s); }
+    __device__ float cap_whole(float s) const { return cap * tanh_of(s, quick); }
     // The bias of a key that far away (past 2^24 to float32's rounding).
     __device__ float bend(float s, float distance) const {
         return fmaf(-slope, fabsf(distance), s);

@@ -1,6 +1,7 @@
 """Attention with rules where numbers leave float32 or its middle, in every
 kernel (few rows, drafts, many rows) and type: scales of pages that are not
-finite under a cap, factors past float32."""
+finite under a cap, factors past float32, caps far above and below the
+scores."""
 import numpy as np
 import pytest
 
@@ -91,3 +92,59 @@ def test_factors_past_float32_with_large_scales(rows, dtype):
             assert np.all(np.abs(out - ref) <= tol + ROUND[dtype][0] * np.abs(ref) + ROUND[dtype][1])
             assert np.all(np.abs(lse - rlse) <= (length / 8 + 64) * U + 8 * U * np.abs(rlse))
         assert np.isfinite(out).all() and np.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("cap", [256.0, 257.0, 1e4, 1e6, 1e8, 1e30])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", ROWS)
+def test_caps_far_above_the_scores(rows, dtype, cap):
+    """A cap that no score comes near changes none.  A score's error: its
+    float32 sum (dim + 24 roundings, query rows of float32 in 22 bits), the
+    cap's: of 16-bit types up to 256 8 u cap (as in the tests of caps there),
+    beyond and in float32 relative to the score, which is at most `size`: 2 for
+    the factor, 2 for the series, 16 where (1 - e) / (1 + e) takes over at 0.25
+    (the difference is off by 4 u of 0.24).  The factor over the cap may fall
+    below float32's normal numbers: 2^-149 of it times a product of at most
+    2^15 * 127 * dim, twice."""
+    announce(f"attn_rules_q8 cap {cap}, {rows} rows {dtype}")
+    length = 333
+    c = Cache(70, [length], 2, 64, 32)
+    c.poison_unused()
+    for gain in (0.3, 2.0, 8.0):
+        q, qf = _typed(np.random.default_rng(5).normal(size=(rows, 4, 64)) * gain, dtype)
+        out, lse = _call(c, q, [rows], cap=cap)
+        cap32 = float(np.float32(cap))
+        ref, rlse, weight, size, _ = X.attention(qf, c.k8, c.ks, c.v8, c.vs, c.table, _cu([rows]), [length], 32,
+                                                 0.125, cap=cap32)
+        ds = (64 + 24 + 20) * U * size + (2.0 ** -21 * size if dtype == "f32" else 0)
+        ds = ds + (8 * U * cap if dtype != "f32" and cap <= 256 else cap * 2.0 ** -148 * 2 ** 15 * 127 * 64)
+        dp = 2 * np.expm1(ds) + (length / 8 + 64) * U + (2.0 ** -21 if dtype == "f32" else 2.0 ** -11)
+        tol = dp[:, :, None] * weight + ROUND[dtype][0] * np.abs(ref) + ROUND[dtype][1]
+        # (values below 2^-40 of the largest may count as 0)
+        tol = tol + 2.0 ** -40 * 127 * length * np.nanmax(c.vs) + 1e-30
+        assert ds.max() < 0.05  # the tolerance says something
+        assert np.all(np.abs(out - ref) <= tol)
+        assert np.all(np.abs(lse - rlse) <= ds + (length / 8 + 64) * U + 8 * U * np.abs(rlse))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", ROWS)
+def test_caps_far_below_the_scores(rows, dtype):
+    """Every score is the cap or its negative but for what tanh leaves: with
+    caps of 1e-30 and 1e-3 at most 2 caps apart, so the scores' error is at
+    most 8 u cap and the rest is the probabilities' and the sums'."""
+    announce(f"attn_rules_q8 small caps, {rows} rows {dtype}")
+    length = 333
+    c = Cache(71, [length], 2, 64, 32)
+    c.poison_unused()
+    q, qf = _typed(np.random.default_rng(5).normal(size=(rows, 4, 64)) * 4, dtype)
+    for cap in (1e-30, 1e-3):
+        out, lse = _call(c, q, [rows], cap=cap)
+        ref, rlse, weight, size, _ = X.attention(qf, c.k8, c.ks, c.v8, c.vs, c.table, _cu([rows]), [length], 32,
+                                                 0.125, cap=float(np.float32(cap)))
+        # a score's own error moves the capped one by at most as much, and by 2 caps
+        ds = np.minimum((64 + 24) * U * size + (2.0 ** -21 * size if dtype == "f32" else 0), 2 * cap) + 8 * U * cap
+        dp = 2 * np.expm1(ds) + (length / 8 + 64) * U + (2.0 ** -21 if dtype == "f32" else 2.0 ** -11)
+        tol = dp[:, :, None] * weight + ROUND[dtype][0] * np.abs(ref) + ROUND[dtype][1] + 1e-30
+        assert np.all(np.abs(out - ref) <= tol + 2.0 ** -40 * 127 * length * np.nanmax(c.vs))
+        assert np.all(np.abs(lse - rlse) <= ds + (length / 8 + 64) * U + 8 * U * np.abs(rlse))
