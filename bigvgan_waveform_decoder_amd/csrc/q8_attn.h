@@ -223,7 +223,12 @@ struct Shape {
     __device__ Shape(const AttnRules& x, const Row& r)
         : cap(x.cap * kLog2e), slope(0.0f), capped(x.cap > 0.0f), sloped(x.slopes != nullptr),
           quick(sizeof(T) < 4 && x.cap > 0.0f && x.cap <= 256.0f) {
-        if (sloped) slope = x.slopes[r.q_head] * kLog2e;
+        // held at 2^96: its product with a distance below 2^31 stays in float32,
+        // and an infinite slope would be NaN at the row's own place (a NaN stays)
+        if (sloped) {
+            slope = x.slopes[r.q_head] * kLog2e;
+            if (fabsf(slope) > 0x1p96f) slope = copysignf(0x1p96f, slope);
+        }
     }
     // The factor of a page's scores.  A scale that is not finite makes them NaN
     // whatever the cap (`held` alone would make a number of a NaN), and under

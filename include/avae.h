@@ -747,7 +747,8 @@ int avae_kv_write_rope_q8(const void* k, long long k_tok, long long k_head, cons
  * here, and so is what it says of precision and NaN), with rules:
  *   cap > 0: scores become cap * tanh(score / cap).
  *   slopes [q_heads] float32 or NULL: then slope * |p - t| is taken off the
- *     score of key t for the row at place p.  Finite, of either sign.
+ *     score of key t for the row at place p.  Finite, of either sign (past
+ *     5e28 in magnitude as 5e28: nothing but the nearest or farthest key is left).
  *   prefix [seqs] int32 or NULL (causal only): keys t < prefix[b] are seen by
  *     every row of sequence b, whatever its place and the window are: with a
  *     window those keys and the window's.  max_prefix: at least the largest

@@ -1,7 +1,7 @@
 """Attention with rules where numbers leave float32 or its middle, in every
 kernel (few rows, drafts, many rows) and type: scales of pages that are not
 finite under a cap, factors past float32, caps far above and below the
-scores."""
+scores, slopes as large as float32 holds."""
 import numpy as np
 import pytest
 
@@ -148,3 +148,40 @@ def test_caps_far_below_the_scores(rows, dtype):
         tol = dp[:, :, None] * weight + ROUND[dtype][0] * np.abs(ref) + ROUND[dtype][1] + 1e-30
         assert np.all(np.abs(out - ref) <= tol + 2.0 ** -40 * 127 * length * np.nanmax(c.vs))
         assert np.all(np.abs(lse - rlse) <= ds + (length / 8 + 64) * U + 8 * U * np.abs(rlse))
+
+
+# ------------------------------------------------------------------ slopes
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", ROWS)
+def test_slopes_as_large_as_float32_holds(rows, dtype, cap):
+    """Slopes are finite, of either sign: the nearest key alone is left, or
+    the farthest, and nothing becomes NaN where slope * log2 e or the product
+    with the distance passes float32.  The output is one value row: 8 bits
+    times a scale, off by the weight's rounding and its own."""
+    announce(f"attn_rules_q8 slopes at float32's end, {rows} rows {dtype}")
+    length = 300
+    c = Cache(72, [length], 2, 64, 16)
+    c.poison_unused()
+    q, qf = _typed(np.random.default_rng(5).normal(size=(rows, 4, 64)), dtype)
+    slopes = np.array([3.4e38, -3.4e38, 1e30, -1e37], np.float32)
+    out, lse = _call(c, q, [rows], slopes=slopes, cap=cap)
+    v = (c.v8.astype(np.float64) * c.vs[:, :, None, None])[c.table[0]].transpose(1, 0, 2, 3).reshape(2, -1, 64)
+    ref, rlse, _, size, _ = X.attention(qf, c.k8, c.ks, c.v8, c.vs, c.table, _cu([rows]), [length], 16, 0.125,
+                                        cap=cap, slopes=slopes)
+    pos = np.arange(length - rows, length)
+    for h, at in ((0, pos), (1, 0 * pos), (2, pos), (3, 0 * pos)):
+        want = v[h // 2][at]
+        part = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -21
+        tol = (part + 64 * U + ROUND[dtype][0]) * np.abs(want) + ROUND[dtype][1]
+        tol = tol + 2.0 ** -40 * 127 * np.nanmax(c.vs) * length
+        assert np.all(np.abs(out[:, h] - want) <= tol), h
+        assert np.isfinite(lse[:, h]).all()
+        if h in (0, 2):  # the key at the row itself: its score
+            near = (64 + 24) * U * size[:, h] + (2.0 ** -21 * size[:, h] if dtype == "f32" else 0) + 8 * U * cap
+            assert np.all(np.abs(lse[:, h] - rlse[:, h]) <= near + 64 * U + 8 * U * np.abs(rlse[:, h]))
+    slopes[1] = np.nan
+    out, lse = _call(c, q, [rows], slopes=slopes, cap=cap)
+    assert np.array_equal(np.isnan(out).all((0, 2)), [False, True, False, False])
+    assert np.array_equal(np.isnan(lse).any(0), [False, True, False, False])
