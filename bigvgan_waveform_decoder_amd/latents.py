@@ -117,8 +117,11 @@ class LatentGenerator:
                   for k, v in weights.items()}
         self.pos = positions(max_frames, cfg.width, dev).bfloat16()
         pages = -(-max_frames // cfg.page)
-        self.caches = [avae.KvCacheQ8.empty(streams * pages, cfg.kv_heads, cfg.page, cfg.dim, dev)
-                       for _ in range(cfg.layers)]
+        # keys, values and their scales, all layers in one: a page of all of them is one copy
+        shape = (cfg.layers, streams * pages, cfg.kv_heads, cfg.page, cfg.dim)
+        self.held = (*(torch.zeros(shape, dtype=torch.int8, device=dev) for _ in range(2)),
+                     *(torch.zeros(shape[:3], device=dev) for _ in range(2)))
+        self.caches = [avae.KvCacheQ8(*(t[i] for t in self.held)) for i in range(cfg.layers)]
         self.table = torch.arange(streams * pages, dtype=torch.int32, device=dev).view(streams, pages)
         self.lens = torch.zeros(streams, dtype=torch.int32, device=dev)
         self.one_each = torch.arange(streams + 1, dtype=torch.int32, device=dev)
@@ -156,6 +159,13 @@ class LatentGenerator:
             avae.kv_write_rope_q8(self.caches[i], k, v, self.table, cu, lens, self.rope,
                                   k_weight=self.w.get(f"{i}.k_norm"), eps=self.cfg.eps,
                                   positions=positions, max_new=most)
+
+    def _tails(self):
+        """The page of each stream that its next frame goes into (its last
+        one where all are full), and what the caches hold there."""
+        col = (self.lens.long() // self.cfg.page).clamp(max=self.table.shape[1] - 1)
+        pages = self.table.long().gather(1, col[:, None])[:, 0]
+        return pages, [t[:, pages] for t in self.held]
 
     def _forward(self, frames, cu, lens, most: int, longest: int, tree=None, positions=None):
         """frames [rows, c_latent] float32, the streams' last ones as cu and
@@ -231,7 +241,13 @@ class LatentGenerator:
         """Drafted frames [n, c_latent] of each stream (n may be 0), draft i
         following draft parents[i] < i of its stream or, with -1, the stream's
         last frame -> the next frame after each draft, [n, c_latent] a stream.
-        The streams stay where they are: keep() goes on."""
+        The streams stay where they are, to the bit: keep() goes on.
+
+        While they are checked the drafts lie in the cache behind their
+        stream's frames, in pages of one scale a head: the larger a draft, the
+        coarser what shares its page, and one that is not finite makes the
+        answers after its stream's drafts so.  The pages that held frames
+        before are put back as they were."""
         cfg = self.cfg
         if self.empty:
             raise ValueError("a prompt comes first")
@@ -256,8 +272,13 @@ class LatentGenerator:
             lens = self.lens + (cu[1:] - cu[:-1])
             up = torch.tensor([p for u in parents for p in u], dtype=torch.int32, device=dev)
             tree, positions = avae.tree_mask(up, cu, lens, max_rows=most)
-            y, kept = self._forward(torch.cat([d.float() for d in drafts]).to(dev).contiguous(), cu,
-                                    lens, most, longest, tree, positions)
+            pages, held = self._tails()
+            try:
+                y, kept = self._forward(torch.cat([d.float() for d in drafts]).to(dev).contiguous(), cu,
+                                        lens, most, longest, tree, positions)
+            finally:
+                for t, was in zip(self.held, held):
+                    t[:, pages] = was
         self.drafts = (parents, kept)
         return list(y.split(new))
 
