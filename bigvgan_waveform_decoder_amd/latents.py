@@ -170,7 +170,8 @@ class LatentGenerator:
     def _forward(self, frames, cu, lens, most: int, longest: int, tree=None, positions=None):
         """frames [rows, c_latent] float32, the streams' last ones as cu and
         lens say (at their places, or drafts at `positions` that see each other
-        by `tree`) -> [rows, c_latent], and keys and values a layer."""
+        by `tree`) -> [rows, c_latent], and the drafts' keys and values a layer
+        (none without `tree`)."""
         cfg, bf16 = self.cfg, torch.bfloat16
         rows = frames.shape[0]
         at = positions
@@ -194,7 +195,8 @@ class LatentGenerator:
                                          positions=positions, cu=cu, lens=lens, max_rows=most,
                                          inplace=True)
             self._write(i, k, v, cu, lens, most, positions)
-            kept.append((k, v))
+            if tree is not None:
+                kept.append((k, v))
             a = self._attend(q, cache, cu, lens, most, longest, tree)
             delta = self._linear(*avae.quant_q8(a.flatten(1)), f"{i}.o", dtype=bf16)
             q8, s, h = avae.rms_norm_q8(delta, self.w[f"{i}.norm2"], cfg.eps, residual=h)

@@ -1,5 +1,5 @@
 """What checked drafts leave behind in a latent generator: nothing, unless
-they are kept."""
+they are kept; and what a generator holds."""
 import pytest
 
 from tests.gpu_util import announce
@@ -67,3 +67,23 @@ def test_kept_drafts_are_written_over_what_was_there():
     # the first layer's keys of the kept draft have the range of a frame, not of the large one
     page = a.table[0, 1]
     assert bool((a.caches[0].k_scale[page] <= 4 * before[0][2][page]).all())
+
+
+def test_a_prompt_keeps_no_rows():
+    """The packed product of a layer is gone when the next one's is made: more
+    layers, the same memory beside weights and cache."""
+    import torch
+    from bigvgan_waveform_decoder_amd.latents import LatentGenerator, random_weights
+    announce("memory of a prompt")
+    rows, need = 3000, []
+    for layers in (2, 8):
+        cfg = _config(rot=64, layers=layers)
+        gen = LatentGenerator(cfg, random_weights(cfg, 3), 1, rows + 1)
+        x = torch.zeros((rows, cfg.c_latent), device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        was = torch.cuda.memory_allocated()
+        gen.prefill([x])
+        need.append(torch.cuda.max_memory_allocated() - was)
+        del gen
+    assert need[1] - need[0] < rows * cfg.qkv * 2
