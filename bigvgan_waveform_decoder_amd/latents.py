@@ -125,7 +125,7 @@ class LatentGenerator:
         self.table = torch.arange(streams * pages, dtype=torch.int32, device=dev).view(streams, pages)
         self.lens = torch.zeros(streams, dtype=torch.int32, device=dev)
         self.one_each = torch.arange(streams + 1, dtype=torch.int32, device=dev)
-        self.counts = [0] * streams  # what lens holds, on the host
+        self.counts = [0] * streams  # what lens holds, on the host (or what bounds it)
         self.empty = True
         self.rope = avae.Rope.of(cfg.rot, theta=cfg.theta, device=dev) if cfg.rot else None
         self.prompt = torch.zeros(streams, dtype=torch.int32, device=dev)
@@ -134,7 +134,12 @@ class LatentGenerator:
 
     @property
     def longest(self) -> int:
+        """The most frames that a stream has; set by who sets `lens` back."""
         return max(self.counts)
+
+    @longest.setter
+    def longest(self, frames: int) -> None:
+        self.counts = [frames] * self.streams  # (at most: lens has each stream's)
 
     def _linear(self, q, scale, name, **kw):
         w, w_scale = self.w[name]

@@ -69,6 +69,38 @@ def test_kept_drafts_are_written_over_what_was_there():
     assert bool((a.caches[0].k_scale[page] <= 4 * before[0][2][page]).all())
 
 
+def test_a_generator_starts_over():
+    """`longest` and `empty` set by a caller, new prompts after that: the same
+    bits as from a new generator."""
+    import torch
+    announce("a generator starts over")
+    make, rand = _start(dict(rot=64))
+    a = make()
+    a.check([rand(1)] * 4, [[-1]] * 4)
+    for _ in range(20):
+        a.step(rand(4))
+    a.lens.zero_()
+    a.longest = 0
+    a.empty = True
+    assert a.longest == 0
+    prompts = [rand(n) for n in (3, 20, 40, 7)]
+    x = a.prefill(prompts)
+    b = make()
+    b.lens.zero_()
+    b.longest, b.empty = 0, True
+    assert torch.equal(b.prefill(prompts), x)
+    frame = rand(4)
+    assert torch.equal(a.step(frame), b.step(frame))
+    # streams set back: lengths on the device, the longest of them on the host
+    a.lens.fill_(3)
+    a.longest = 3
+    y = a.step(frame)
+    assert a.longest == 4 and a.lens.tolist() == [4] * 4 and bool(torch.isfinite(y).all())
+    a.check([rand(70)] * 4, [[-1] * 70] * 4)
+    with pytest.raises(ValueError):
+        a.check([rand(77)] * 4, [[-1] * 77] * 4)
+
+
 def test_a_prompt_keeps_no_rows():
     """The packed product of a layer is gone when the next one's is made: more
     layers, the same memory beside weights and cache."""
