@@ -225,6 +225,7 @@ class LatentGenerator:
         cu = torch.tensor([0] + counts, dtype=torch.int32, device=dev).cumsum(0).int()
         self.lens.copy_(torch.tensor(counts, dtype=torch.int32))
         self.counts, self.empty = counts, False
+        self.drafts = None
         self.prompt.copy_(self.lens)
         self.longest_prompt = self.longest
         y, _ = self._forward(torch.cat([p.float() for p in prompts]).to(dev).contiguous(), cu, self.lens,

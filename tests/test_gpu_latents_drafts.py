@@ -71,7 +71,7 @@ def test_kept_drafts_are_written_over_what_was_there():
 
 def test_a_generator_starts_over():
     """`longest` and `empty` set by a caller, new prompts after that: the same
-    bits as from a new generator."""
+    bits as from a new generator; drafts of before are forgotten."""
     import torch
     announce("a generator starts over")
     make, rand = _start(dict(rot=64))
@@ -79,12 +79,15 @@ def test_a_generator_starts_over():
     a.check([rand(1)] * 4, [[-1]] * 4)
     for _ in range(20):
         a.step(rand(4))
+    a.check([rand(1)] * 4, [[-1]] * 4)
     a.lens.zero_()
     a.longest = 0
     a.empty = True
     assert a.longest == 0
     prompts = [rand(n) for n in (3, 20, 40, 7)]
     x = a.prefill(prompts)
+    with pytest.raises(ValueError):
+        a.keep([[0]] * 4)  # those were the old streams'
     b = make()
     b.lens.zero_()
     b.longest, b.empty = 0, True
