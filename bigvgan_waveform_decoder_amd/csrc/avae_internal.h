@@ -221,7 +221,8 @@ struct AttnQ8 {
 size_t attn_q8_workspace_bytes(int seqs, int total, int max_rows, int max_len, int q_heads,
                                int heads, int dim, int elem, int window, int prefix = 0,
                                bool rules = false);
-// Workgroups of 256 threads that the largest of its launches has.
+// Threads of its largest launch in units of 256, over all axes: those of the
+// kernel, or of the join.
 long long attn_q8_workgroups(int seqs, int total, int max_rows, int max_len, int q_heads,
                              int heads, int dim, int elem, int window, int prefix = 0,
                              bool rules = false);

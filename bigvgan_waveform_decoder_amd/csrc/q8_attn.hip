@@ -14,11 +14,15 @@ long long attn_q8_workgroups(int seqs, int total, int max_rows, int max_len, int
                              int heads, int dim, int elem, int window, int prefix,
                              bool rules) {
     const Cut k = cut(seqs, max_rows, max_len, q_heads, heads, dim, elem, window, prefix, rules);
+    const int wide = k.mid ? mid_wide_waves(dim) : wide_waves(dim, elem);
     const long long blocks =
-        k.mid ? mid_blocks(k, heads, seqs) : (long long)k.tiles * k.splits * heads * seqs;
-    const long long rows = (long long)total * q_heads;
+        (k.mid ? mid_blocks(k, heads, seqs) : (long long)k.tiles * k.splits * heads * seqs) *
+        (k.wide ? wide / kWaves : 1);
     if (k.splits == 1) return blocks;
-    return std::max(blocks, join_by_waves(k.splits, rows) ? rows / 4 + 1 : 2 * rows);
+    // a join with rules goes by the sequences, as many rows for each as one may have
+    const long long rows = (long long)total * q_heads;
+    const long long joined = rules ? (long long)max_rows * q_heads * seqs : rows;
+    return std::max(blocks, join_by_waves(k.splits, rows) ? joined / 4 + 1 : 2 * joined);
 }
 
 hipError_t launch_attn_q8(int dtype, const AttnQ8& a, const CacheQ8& c, const Ragged& r, void* ws,
