@@ -526,10 +526,10 @@ hipError_t qk(const HeadsQ8& q, const HeadsQ8& k, const RopeQ8& rope, const Ragg
     // 16 bytes of a's and 16 of b's a lane, or 8 where heads are too short
     constexpr int P = 16 / sizeof(T);
     const Lie whole = lie_of(rope, dim, P), half = lie_of(rope, dim, 4);
-    if (whole != kAnyhow)
-        with_lie(whole, [&](auto lie) {
-            turn_heads<T, P, decltype(lie)::value>(q, k, rope, r, dim, eps, stream);
-        });
+    if (whole == kRuns)
+        turn_heads<T, P, kRuns>(q, k, rope, r, dim, eps, stream);
+    else if (whole == kNeighbours)
+        turn_heads<T, P, kNeighbours>(q, k, rope, r, dim, eps, stream);
     else
         with_lie(half, [&](auto lie) {
             turn_heads<T, 4, decltype(lie)::value>(q, k, rope, r, dim, eps, stream);
