@@ -242,5 +242,8 @@ struct AttnRules {
 };
 hipError_t launch_attn_rules_q8(int dtype, const AttnQ8& a, const AttnRules& x, const CacheQ8& c,
                                 const Ragged& r, void* ws, hipStream_t stream);
+// The same for 16-bit types under caps over 256.
+hipError_t launch_attn_caps_q8(int dtype, const AttnQ8& a, const AttnRules& x, const CacheQ8& c,
+                               const Ragged& r, void* ws, hipStream_t stream);
 
 }  // namespace avae

@@ -1,5 +1,5 @@
 // Attention over the 8-bit paged cache: the kernels, for the plain form and
-// the one with rules (q8_attn.hip, q8_attn_rules.hip).
+// the one with rules (q8_attn.hip, q8_attn_rules.hip, q8_attn_caps.hip).
 //
 // For a query row at position p of its sequence, over the keys t it sees
 // (first <= t <= p, t > p - window):
@@ -122,6 +122,18 @@ struct NoRules {};
 template <typename R>
 constexpr bool kRules = !std::is_same<R, NoRules>::value;
 
+// Rules with a cap that 16-bit scores may lie far below: it is taken to the
+// scores' own rounding, as float32's is.  Kernels of their own, since the
+// others' registers are full (both in one, the capped prompts of [3849 rows,
+// 6047 keys] and [3642, 4762] take 354 us for 335, trees of heads of 256 230 for
+// 213; these kernels take 460 for such a prompt).
+struct FineRules : AttnRules {
+    explicit FineRules(const AttnRules& x) : AttnRules(x) {}
+};
+constexpr float kQuickCap = 256.0f;  // caps above it
+template <typename T, typename R>
+constexpr bool kQuick = sizeof(T) < 4 && !std::is_same<R, FineRules>::value;
+
 // What a tile of 16 query rows sees.  Rows are the sequence's new tokens
 // times the query heads of one cache head; lane 16 g + n has row n.
 struct Row {
@@ -192,15 +204,18 @@ __device__ inline unsigned keys_seen(const Row& r, const AttnRules& x, int start
     return seen | (ones_below(r.pre - t) & ~ones_below(r.first - t));
 }
 
-// tanh(y): (1 - e) / (1 + e) with e = exp(-2 |y|) is 2^-24 off, and a cap
-// multiplies that.  `rough`: let it (16-bit types under caps up to 256, whose
-// own rounding hides it); else small |y| take the odd series, right to y's own
-// rounding, so that a score far below its cap stays what it is.  (Without it a
-// cap of 1e6 made bfloat16 scores 1.3% wrong, one of 1e30 all of them 0.)
-__device__ inline float tanh_of(float y, bool rough) {
+// tanh(y) as (1 - e) / (1 + e) with e = exp(-2 |y|): 2^-24 off, and a cap
+// multiplies that, which the rounding of 16-bit types hides up to caps of 256.
+__device__ inline float tanh_far(float y) {
     const float e = __builtin_amdgcn_exp2f(fabsf(y) * (-2.0f * kLog2e));
-    const float far = copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), y);
-    if (rough) return far;
+    return copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), y);
+}
+
+// Small |y| by the odd series, right to y's own rounding, so that a score far
+// below its cap stays what it is.  (Without it a cap of 1e6 made bfloat16
+// scores 1.3% wrong, one of 1e30 all of them 0.)
+__device__ inline float tanh_of(float y) {
+    const float far = tanh_far(y);
     const float z = y * y;
     float p = fmaf(z, -8.8632355e-3f, 2.1869489e-2f);
     p = fmaf(z, p, -5.3968254e-2f);
@@ -211,18 +226,17 @@ __device__ inline float tanh_of(float y, bool rough) {
 
 // Scores in units of log2 e from products and what they are multiplied with:
 // their factor over the cap where there is one.
-template <typename T>
+template <typename T, typename R>
 struct Shape {
     float cap, slope;  // in units of log2 e; the slope is the row's
     bool capped, sloped;
     // 16-bit types: cap tanh(y) = cap - 2 cap / (1 + exp(2 y)), the first term
     // left out of the scores since all of a row have it; 5 2^-24 cap off,
     // which for caps up to 256 their own rounding hides.
-    bool quick;
+    static constexpr bool quick = kQuick<T, R>;
 
     __device__ Shape(const AttnRules& x, const Row& r)
-        : cap(x.cap * kLog2e), slope(0.0f), capped(x.cap > 0.0f), sloped(x.slopes != nullptr),
-          quick(sizeof(T) < 4 && x.cap > 0.0f && x.cap <= 256.0f) {
+        : cap(x.cap * kLog2e), slope(0.0f), capped(x.cap > 0.0f), sloped(x.slopes != nullptr) {
         // held at 2^96: its product with a distance below 2^31 stays in float32,
         // and an infinite slope would be NaN at the row's own place (a NaN stays)
         if (sloped) {
@@ -246,16 +260,16 @@ struct Shape {
         return __builtin_amdgcn_rcpf(-1.0f - __builtin_amdgcn_exp2f(s));
     }
     // of s = y
-    __device__ float cap_whole(float s) const { return cap * tanh_of(s, quick); }
+    __device__ float cap_whole(float s) const { return cap * (quick ? tanh_far(s) : tanh_of(s)); }
     // The bias of a key that far away (past 2^24 to float32's rounding).
     __device__ float bend(float s, float distance) const {
         return fmaf(-slope, fabsf(distance), s);
     }
 };
 
-template <typename T>
-__device__ inline Shape<T> shape_of(const AttnRules& x, const Row& r) {
-    return Shape<T>(x, r);
+template <typename T, typename R>
+__device__ inline Shape<T, R> shape_of(const R& x, const Row& r) {
+    return Shape<T, R>(x, r);
 }
 template <typename T>
 __device__ inline NoRules shape_of(const NoRules&, const Row&) {
@@ -628,9 +642,9 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 
 // Scores of 32 keys by the rules, as the exponential takes them: s * by, a
 // factor for each 16.  `away`: the row's distance from the lane's first key.
-template <typename T>
-__device__ inline void shape_scores(const Shape<T>& shape, f16v& s, float* by, float away) {
-    if (shape.quick) {
+template <typename T, typename R>
+__device__ inline void shape_scores(const Shape<T, R>& shape, f16v& s, float* by, float away) {
+    if (shape.quick && shape.capped) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             by[u] *= 2.0f * kLog2e;
@@ -1084,7 +1098,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_ke
     l = (l + __shfl_xor(l, 32)) * 0x1p-15f;
     if (!row.live) return;
     if constexpr (kRules<R>)
-        if (shape.quick) m += shape.cap;
+        if (shape.quick && shape.capped) m += shape.cap;
     const long long out_row = (long long)row.tok * a.q_heads + row.q_head;
     // the unit in two halves, since it may be below float32
     const float half = __builtin_amdgcn_exp2f(0.5f * (lg_run - 15.0f));
@@ -1365,10 +1379,10 @@ hipError_t run(const AttnQ8& a, R x, const CacheQ8& c, const Ragged& r, float* p
         const dim3 grid((unsigned)(k.mid ? mid_blocks(k, c.heads, r.seqs) : blocks));
         constexpr int W = wide_waves(D, sizeof(T)), MW = mid_wide_waves(D);
         if (k.mid && k.wide)
-            hipLaunchKernelGGL((attn_q8_mid_kernel<T, D, MW>), grid, dim3(64 * MW), 0, stream, a, c,
+            hipLaunchKernelGGL((attn_q8_mid_kernel<T, D, R, MW>), grid, dim3(64 * MW), 0, stream, a, c,
                                r, x, k.splits, k.chunk, k.tiles, part);
         else if (k.mid)
-            hipLaunchKernelGGL((attn_q8_mid_kernel<T, D, kWaves>), grid, dim3(64 * kWaves), 0,
+            hipLaunchKernelGGL((attn_q8_mid_kernel<T, D, R, kWaves>), grid, dim3(64 * kWaves), 0,
                                stream, a, c, r, x, k.splits, k.chunk, k.tiles, part);
         else if (k.wide)
             hipLaunchKernelGGL((attn_q8_few_kernel<T, D, R, W>), grid, dim3(64 * W), 0, stream, a,
@@ -1416,9 +1430,13 @@ hipError_t launch_attn(int dtype, const AttnQ8& a, const R& x, const CacheQ8& c,
                        void* ws, const char* name, hipStream_t stream) {
     prof_pre(stream);
     float* part = (float*)ws;
-    const hipError_t e = dtype == AVAE_F32    ? attn_q8<float>(a, x, c, r, part, stream)
-                         : dtype == AVAE_BF16 ? attn_q8<__bf16>(a, x, c, r, part, stream)
-                                              : attn_q8<_Float16>(a, x, c, r, part, stream);
+    hipError_t e = hipErrorInvalidValue;
+    if (dtype == AVAE_BF16)
+        e = attn_q8<__bf16>(a, x, c, r, part, stream);
+    else if (dtype == AVAE_F16)
+        e = attn_q8<_Float16>(a, x, c, r, part, stream);
+    else if constexpr (!std::is_same<R, FineRules>::value)
+        e = attn_q8<float>(a, x, c, r, part, stream);
     // lengths are on the device: counted as if every row saw max_len keys
     const double pairs = (double)r.total * a.q_heads * a.max_len;
     prof_post(stream, name, 4.0 * pairs * c.dim,

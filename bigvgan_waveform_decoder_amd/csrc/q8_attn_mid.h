@@ -44,9 +44,9 @@ __device__ inline Words<(N + 3) / 4> load_bytes(const int8_t* p) {  // N bytes, 
     }
 }
 
-template <typename T, int D, int W>
+template <typename T, int D, typename R, int W>
 __global__ __launch_bounds__(64 * W, W > kWaves ? 2 : mid_residency(D)) void attn_q8_mid_kernel(
-    AttnQ8 a, CacheQ8 c, Ragged r, AttnRules x, int splits, int chunk, int tiles, float* part) {
+    AttnQ8 a, CacheQ8 c, Ragged r, R x, int splits, int chunk, int tiles, float* part) {
     constexpr bool kSplit = sizeof(T) == 4;
     constexpr int KC = D / 16;  // key operands of 16 dims
     constexpr int DT = D / 32;  // output tiles; a lane's values of one key, too
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(64 * W, W > kWaves ? 2 : mid_residency(D)) void att
     fetch_values();
     look_up(u_first + 32 * W);
 
-    const Shape<T> shape(x, row);
+    const Shape<T, R> shape(x, row);
     // The rows are the same for all waves: their operands lie in LDS, in the
     // lanes' order, and leave the registers to another wave.
     float to_log2;  // not negative: the scale's sign goes into the rows
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(64 * W, W > kWaves ? 2 : mid_residency(D)) void att
     }
 
     l = (l + __shfl_xor(l, 32)) * 0x1p-15f;
-    if (shape.quick) m += shape.cap;
+    if (shape.quick && shape.capped) m += shape.cap;
     if (g == 0) {
         s_m[wave * 32 + n32] = m;
         s_l[wave * 32 + n32] = l;

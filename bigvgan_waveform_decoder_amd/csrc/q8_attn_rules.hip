@@ -6,6 +6,8 @@ namespace avae {
 
 hipError_t launch_attn_rules_q8(int dtype, const AttnQ8& a, const AttnRules& x, const CacheQ8& c,
                                 const Ragged& r, void* ws, hipStream_t stream) {
+    if (dtype != AVAE_F32 && x.cap > kQuickCap)
+        return launch_attn_caps_q8(dtype, a, x, c, r, ws, stream);
     return launch_attn(dtype, a, x, c, r, ws, "attn_rules_q8_kernel", stream);
 }
 
