@@ -558,7 +558,11 @@ __global__ __launch_bounds__(64 * W, few_residency(D, sizeof(T), W)) void attn_q
             for (int i = 0; i < 4; ++i) {
                 const float p = __builtin_amdgcn_exp2f(s[h][i] - m_at);
                 l += p;
-                const float x = p * pv;
+                float x = p * pv;
+                // both parts are of this number: the product would else be
+                // fused with one conversion and not with the other, 2^-11 apart
+                // where its rounding makes a tie
+                if (kTwoParts<T>) asm("" : "+v"(x));
                 const _Float16 hx = (_Float16)x;
                 ph[4 * h + i] = hx;
                 if (kTwoParts<T>) pl[4 * h + i] = (_Float16)(x - (float)hx);
