@@ -1449,7 +1449,7 @@ def attn_rules_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = N
     """avae_attn_rules_q8: attn_q8 with scores capped (cap > 0), biased by
     distance (slopes [q_heads] float32), and the first prefix [seqs] int32
     tokens in view of every row.  max_prefix: at least the longest prefix
-    (max_len if not given)."""
+    (max_len if not given; beside a window, the keys are cut for as many)."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return attn_rules_q8(q, cache, table, cu, lens, max_q, max_len, scale, causal, window,
@@ -1469,8 +1469,8 @@ def attn_rules_q8(q, cache: KvCacheQ8, table, cu, lens, max_q: Optional[int] = N
 def tree_mask(parents, cu, lens, max_rows: Optional[int] = None, stream=None):
     """avae_tree_mask: parents [tokens] int32 -> (mask [tokens, words] int32
     with a bit for each draft that a draft sees, positions [tokens] int32).
-    max_rows: at least the most drafts of one sequence (all of them if not
-    given); the mask has a word for every 32 of them."""
+    max_rows: at least the most drafts of one sequence (all of the call's if
+    not given), 4096 at most; the mask has a word for every 32 of them."""
     if stream is not None:
         with _torch().cuda.stream(stream):
             return tree_mask(parents, cu, lens, max_rows)

@@ -744,9 +744,14 @@ struct alignas(16) Group {
 // 2 x 4096 rows on as many keys, 16 heads of 128, 400-408 us without order
 // (675-687 TFLOP/s), 219-225 causal (620); float16 275-286, float32 303-312
 // (split operands); heads of 64 146; 8 heads of 256 304-319, float32 462: that
-// kernel alone spills, 26 registers a lane to 108 bytes of scratch.  Two
-// workgroups of four waves a CU: one of eight shares the staging but keeps
-// step, 521 against 427 us.
+// kernel alone spills, 26 registers a lane to 108 bytes of scratch (with rules
+// 2).  Two workgroups of four waves a CU: one of eight shares the staging but
+// keeps step, 521 against 427 us.
+//
+// With rules, prompts of 3849 rows after 2198 tokens and of 3642 after 1120, 12
+// heads of 128, bfloat16: a cap and a prefix 335 us (vector unit busy 50%,
+// matrix cores 19%), the prefix alone 278, a window of 2401 beside it 253, biases
+// alone 311; cap and prefix in float16 376, in float32 567.
 template <typename T, int D, typename R>
 __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void attn_q8_many_kernel(AttnQ8 a, CacheQ8 c, Ragged r, R x,
                                                            int splits, int chunk, int tiles,
@@ -1290,12 +1295,14 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
     // first up to about 64 rows: [64 x 4000], 33 rows, 112 / 149.)
     r.many = rows > 32;
     // With rules, the kernel for drafts between them.  This one / the others in
-    // us, bfloat16, 12 over 4 heads of 128, drafts of one size: [16 x 12000
-    // keys] 24 rows 49 / 83, 48 rows 75 / 79, 96 rows 101 / 95, 192 rows 172 /
-    // 160, 258 rows 236 / 233; [64 x 4000] 24 rows 56 / 100, 96 rows 138 / 126;
-    // [16 x 500 to 24000] 48 rows 97 / 117, 96 rows 142 / 156, 192 rows 222 /
-    // 284, drafts of 99 to 192 rows 184 / 225; [16 x 12000], 96 rows of heads
-    // of 64 75 / 75, of 256 102 / 168, float32 124 / 130.
+    // us on the device, bfloat16, 12 over 4 heads of 128, drafts of one size:
+    // [16 x 12000 keys] 24 rows 51 / 82, 48 rows 71 / 76, 96 rows 91 / 89, 192
+    // rows 154 / 147; [64 x 4000] 24 rows 67 / 99, 96 rows 126 / 116; [16 x 500
+    // to 24000] 48 rows 91 / 132, 96 rows 130 / 144, 192 rows 204 / 257, drafts
+    // of 99 to 192 rows 166 / 211; [16 x 12000], 96 rows of heads of 64 69 / 67,
+    // of 256 176 / 255, float32 117 / 119.  From 96 rows on this one is ahead
+    // where the lengths differ (by up to a quarter) and behind where they are
+    // equal (up to a twelfth), which the host does not see.
     r.mid = rules && rows > 16 && rows <= 192;
     const int height = r.mid ? 32 : r.many ? 32 * kWaves : 16;
     const int step = r.many && !r.mid ? 64 : 32 * kWaves;
@@ -1310,8 +1317,11 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
     // where that is two steps, or where there is nearly one for every CU: no
     // second launch joins chunks.  Whole / split, us for a call, bfloat16, 12
     // over 4 heads of 128: [1 x 300 keys] 15.0 / 19.5, [1 x 700] 15.4 / 19.3,
-    // [1 x 1500] 21.0 / 19.4, [32 x 1500] 22.3 / 22.0, [64 x 1500] 25.1 / 30.1,
-    // [64 x 6000] 78.7 / 86.3.
+    // [1 x 1500] 21.0 / 19.4, [32 x 1500] 22.3 / 22.0; on the device [64 x 1500]
+    // 25 / 31, [64 x 6000] 82 / 90, [64 x 1000 to 2000] 28 / 36, [64 x 200 to
+    // 6000] 54 / 60, but [64 x 200 to 24000] 209 / 200 and one of 24000 among 63
+    // of 500 171 / 98: the longest sequence sets the time, and the lengths are
+    // not known here.
     const int wide = r.mid ? mid_wide_waves(dim) : wide_waves(dim, elem);
     r.wide = rules && (r.mid || !r.many) && pairs <= 256 && r.span > step &&
              (r.span <= 64 * wide || (!r.mid && pairs >= 192));
@@ -1322,14 +1332,14 @@ inline Cut cut(int seqs, int max_rows, int max_len, int q_heads, int heads, int 
     }
     if (r.mid) {
         // One resident round ([16 x 500 to 24000 keys], drafts of 99 to 192
-        // rows: 184 us; two workgroups a CU 193, four 196).
+        // rows: 184 us when measured; two workgroups a CU 193, four 196).
         const int resident = 256 * mid_residency(dim);
         r.chunk = std::max(round_up_to((r.span * pairs + resident - 1) / resident, step), step);
         if (seqs > 1 && seqs <= 64) r.pieces = resident;
     } else if (r.many && rules && r.tiles <= 4) {
         // Drafts over long sequences: cut so that two workgroups a CU have
         // work to the end ([16 x 500 to 24000 keys], drafts of 99 to 192 rows:
-        // 315 us cut by the longest sequence alone, 225 so).
+        // 315 us cut by the longest sequence alone, 225 so, when measured).
         const int resident = 512;
         r.chunk = std::max(round_up_to((r.span * pairs + resident - 1) / resident, step), 256);
         if (seqs > 1 && seqs <= 64) r.pieces = resident;

@@ -15,19 +15,20 @@
 // is one's).
 //
 // One tile is bound by HBM ([16 sequences of 12000 keys, 4 heads of 128], 24
-// rows: 49 us, 4.0 TB/s), more by their vector instructions, 340 for 32 rows
-// and 32 keys, half of them the conversion of keys and values (96 rows 101 us:
-// the vector units are busy 55%, the matrix cores 15% of the cycles; 384
-// accesses of the first cache a step take half of them).  Three waves a SIMD:
-// with the rows' operands in registers there are two (96 rows 110 us); two
+// rows: 51 us, 3.9 TB/s), more by their vector instructions, 370 for 32 rows
+// and 32 keys, half of them the conversion of keys and values (96 rows 91 us:
+// the vector units are busy 65%, the matrix cores 17% of the cycles; 360
+// accesses of the first cache a step).  Three waves a SIMD: with the rows'
+// operands in registers there are two (96 rows 110 us when this took 101); two
 // tiles a wave, which share the conversion and the accesses, leave two at best
-// (144): a wave's step is a chain of instructions, which more waves hide
-// better than fewer instructions shorten it.  Nor do fewer accesses help: keys
-// loaded line by line and turned through LDS take as long (heads of 64, 96
-// rows: 74 us either way).
+// (144 for 101): a wave's step is a chain of instructions, which more waves
+// hide better than fewer instructions shorten it.  Nor do fewer accesses help:
+// keys loaded line by line and turned through LDS take as long (heads of 64,
+// 96 rows: 74 us either way).
 #pragma once
 
-// Waves a SIMD of the kernel below: what its registers allow.
+// Waves a SIMD of the kernel below: what its registers allow (heads of 256
+// nearly: 1 to 7 a lane go to scratch).
 constexpr int mid_residency(int dim) { return dim > 128 ? 2 : 3; }
 // Waves of its workgroups where they take all the keys of their rows: what
 // fits in LDS.

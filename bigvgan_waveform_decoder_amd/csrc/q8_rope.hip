@@ -263,9 +263,11 @@ constexpr int kMaxPairs = 256;  // of a head
 // this wave's own corner.  The next token's heads are on their way meanwhile.
 //
 // Bound by memory: every value is read and written once.  17254 tokens of 16
-// heads of 128 in bfloat16 take 26 us, 5.5 TB/s (47 with 8-byte loads and each
+// heads of 128 in bfloat16 take 26 us, 5.5 TB/s (half of what is read comes from
+// the last-level cache; vector unit busy 53%; 47 with 8-byte loads and each
 // lane's angles made for itself); with 50 dims turned, which no run divides, 38
-// in runs that overlap, 104 one by one.
+// in runs that overlap, 104 one by one: 9 lanes of a head's 16 have work there,
+// 8 of 8 where all is turned.
 template <typename T, int P, Lie LIE>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(HeadsQ8 q, HeadsQ8 k, RopeQ8 rope,
                                                                 Ragged r, int dim, float eps,
@@ -341,11 +343,12 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(HeadsQ8 q, Heads
 // maximum and the one that rounds; HELD 0 (larger pages) makes them twice.
 //
 // The scale is of what is stored, so the page is turned before its maximum is
-// known, in float32: nothing is rounded between.  Bound by memory, with the
-// angles beside it: prompts of 16 heads of 64 in float32, 126 MB in all, take
-// 32 us (3.9 TB/s), the same rows written as they are 24.  One workgroup for
-// the keys of 2 to 16 heads, which makes their angles once, takes 33 to 43: it
-// has its heads after one another, and there are fewer workgroups to hide that.
+// known, in float32: nothing is rounded between.  Bound by vector instructions,
+// the angles' (the unit is busy 85%): prompts of 16 heads of 64 in float32, 126
+// MB in all, take 32 us (3.9 TB/s), the same rows written as they are 24.  One
+// workgroup for the keys of 2 to 16 heads, which makes their angles once, takes
+// 33 to 43: it has its heads after one another, and there are fewer workgroups
+// to hide that.
 template <typename T, int HELD, Lie LIE>
 __global__ __launch_bounds__(kThreads) void kv_write_rope_q8_kernel(
     const T* __restrict__ k, long long k_tok, long long k_head, const T* __restrict__ v,
